@@ -21,7 +21,9 @@
  * where moe_grouped_mlp_fwd is moe_grouped_fc1_swiglu followed by
  * moe_grouped_fc2 (moe_grouped_fc1_swiglu_dense / moe_grouped_fc2_dense run
  * the routed and the shared expert in the same launches). The backward of
- * the routed experts is moe_grouped_mlp_bwd.
+ * the routed experts is moe_grouped_mlp_bwd. The attention beside it is
+ * moe_mla_attn_fwd / moe_mla_attn_bwd (prompts, training) and moe_mla_append
+ * -> moe_mla_decode (serving over a paged latent cache).
  *
  * Conventions for every call
  *   - Pointers are device pointers owned by the caller unless stated; the
@@ -651,6 +653,136 @@ int moe_route_bwd(const void* dout, const void* y, int act_fmt,
  */
 int moe_bias_update(const int32_t* counts, int E, float gamma, const float* bias,
                     float* bias_out, hipStream_t stream);
+
+/*
+ * Latent attention — the attention beside the experts in the layer (TE
+ * DeepSeekV3Layer page, Description, MultiLatentAttention item). One vector
+ * per token is kept for all heads: a latent c of 512 values and a rotary key
+ * kr of 64. Head h's key is (W_UK[h] c | kr), its value W_UV[h] c, W_UK[h]
+ * and W_UV[h] [128, 512]; a query has 128 + 64 values. The calls below run on
+ * bf16 tensors with these sizes (fmt = MOE_BF16; anything else is
+ * MOE_ERR_UNSUPPORTED) and any head count from 1 to 1024. Sums, softmax
+ * statistics and lse are fp32; weights and score gradients are rounded to
+ * bf16 as matrix operands.
+ * *_ld: elements from one token's row to the next (a multiple of 8, at most
+ * 2^23); a token's heads are consecutive. So a tensor may be a slice of wider
+ * rows. scale: positive and finite.
+ * Packed sequences: cu [B + 1] int32 device, sequence b is rows [cu[b],
+ * cu[b + 1]); values are clamped to the tensors, rows outside every sequence
+ * are not written.
+ */
+
+/*
+ * moe_mla_attn_fwd — attention over expanded keys and values (prompts,
+ * training):
+ *   s[i, j] = scale * (q[i, h, :128] . kv[j, h, :128] + q[i, h, 128:] . k_rope[j])
+ *   out[i, h] = sum_j softmax_j(s[i, :]) kv[j, h, 128:]
+ *   lse[i, h] = log sum_j exp s[i, j]
+ * q [Tq, n_heads, 192], kv [Tk, n_heads, 256] (key part, then value), k_rope
+ * [Tk, 64] (shared by the heads), out [Tq, n_heads, 128], lse [Tq, n_heads]
+ * fp32 (optional).
+ * causal   1: query i of a sequence with n_q queries and n_k keys sees keys
+ *          j <= i + n_k - n_q (the last query sees every key); 0: all keys.
+ * A query without keys gives out 0 and lse -inf. A key that is hidden from
+ * some queries of its sequence and shown to others must have a finite value
+ * row: its weight 0 still multiplies it, as in the formula's matrix product.
+ * Limits: Tq and Tk <= 2^28, Tq * n_heads and Tk * n_heads <= 2^27,
+ * B * n_heads <= 2^22. Tq == 0 or B == 0 is a no-op.
+ */
+int moe_mla_attn_fwd(const void* q, int64_t q_ld, const void* kv, int64_t kv_ld,
+                     const void* k_rope, int64_t kr_ld, int fmt, const int32_t* cu_q,
+                     const int32_t* cu_k, int B, int Tq, int Tk, int n_heads,
+                     int causal, float scale, void* out, int64_t out_ld, float* lse,
+                     hipStream_t stream);
+
+/* moe_mla_attn_bwd_workspace — bytes of moe_mla_attn_bwd's workspace: 8 per
+ * query and head, 256 per key and head (0 for bad sizes). */
+size_t moe_mla_attn_bwd_workspace(int Tq, int Tk, int n_heads);
+
+/*
+ * moe_mla_attn_bwd — gradients of moe_mla_attn_fwd, from the gradient dout of
+ * out and the forward's inputs, out and lse:
+ *   dq [Tq, n_heads, 192], dkv [Tk, n_heads, 256], dk_rope [Tk, 64] (summed
+ *   over the heads in fp32), bf16 out; keys that no query sees get 0.
+ * Other arguments and limits as moe_mla_attn_fwd. The results do not depend
+ * on the order in which workgroups run (no atomics).
+ */
+int moe_mla_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q_ld,
+                     const void* kv, int64_t kv_ld, const void* k_rope, int64_t kr_ld,
+                     int fmt, const void* out, int64_t out_ld, const float* lse,
+                     const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk,
+                     int n_heads, int causal, float scale, void* dq, int64_t dq_ld,
+                     void* dkv, int64_t dkv_ld, void* dk_rope, int64_t dkr_ld, void* ws,
+                     size_t ws_bytes, hipStream_t stream);
+
+/*
+ * moe_mla_append — new tokens into the latent cache (serving), per token t:
+ *   cache[slots[t], :512] = c / sqrt(mean(c^2) + eps) * norm_w, c = kv_a[t, :512]
+ *   cache[slots[t], 512:] = rotary(kv_a[t, 512:576])
+ *   q_out[t, h] = (q[t, h, :128] | rotary(q[t, h, 128:]))
+ * rotary turns pair i = (x, y) by the angle of row positions[t]:
+ * (x cos - y sin, x sin + y cos), cos and sin [max_pos, 32] fp32. Pair i is
+ * values (2 i, 2 i + 1) with interleaved = 1, (i, i + 32) with 0.
+ * kv_a     [T, 576] rows kv_ld apart.
+ * norm_w   [512] bf16, or NULL: the latents are stored as they are.
+ * cos, sin both NULL: no rotation (positions is then not read). Positions
+ *          outside [0, max_pos) take the nearest row.
+ * slots    [T] int64: cache row (page * page_size + place) of each token;
+ *          values outside [0, n_slots) write nothing (padding tokens). Two
+ *          tokens with one slot leave either's row.
+ * cache    [n_slots, 576] bf16.
+ * q, q_out [T, n_heads, 192], both NULL or both given; q_out may equal q
+ *          (with qo_ld == q_ld) and must not overlap it otherwise.
+ * Limits: T <= 2^23, eps in [0, 1]. T == 0 is a no-op.
+ */
+int moe_mla_append(const void* kv_a, int64_t kv_ld, int fmt, const void* norm_w,
+                   float eps, const float* cos, const float* sin, int max_pos,
+                   const int32_t* positions, int interleaved, const int64_t* slots,
+                   void* cache, int64_t n_slots, const void* q, int64_t q_ld,
+                   void* q_out, int64_t qo_ld, int T, int n_heads, hipStream_t stream);
+
+/* moe_mla_decode_workspace — bytes of moe_mla_decode's workspace for up to T
+ * new tokens (it grows with T; 0 for bad sizes). */
+size_t moe_mla_decode_workspace(int T, int n_heads);
+
+/*
+ * moe_mla_decode — attention of the last tokens of B requests over a paged
+ * latent cache, in absorbed form (serving: single tokens, drafted tokens,
+ * trees of drafted tokens):
+ *   q_lat = q[t, h, :128] W_UK[h],  s[j] = scale * (q_lat . c_j + q[t, h, 128:] . kr_j)
+ *   out[t, h] = W_UV[h] sum_j softmax_j(s) c_j,  lse[t, h] = log sum_j exp s[j]
+ * The result is moe_mla_attn_fwd's on the expanded keys and values, up to
+ * rounding (q_lat is rounded to bf16 as matrix operand).
+ * q        [T, n_heads, 192] rows q_ld apart: the new tokens of all requests,
+ *          request b's are rows [cu_q[b], cu_q[b + 1]) (cu_q [B + 1] int32).
+ * w_uk     [n_heads, 512, 128] bf16: each W_UK[h] transposed (laid out once);
+ * w_uv     [n_heads, 128, 512] bf16.
+ * cache    [n_pages, page_size, 576] bf16 (moe_mla_append's rows), any
+ *          page_size; page_table [B, max_pages] int32: request b's token j is
+ *          place j % page_size of page page_table[b, j / page_size] (page ids
+ *          outside [0, n_pages) take the nearest page).
+ * lens     [B] int32: tokens of request b in the cache, its n_q new ones
+ *          included as the last; clamped to max_pages * page_size. Rows past
+ *          a request's length are never used, whatever they hold.
+ * tree_mask NULL: new token i sees the earlier tokens and new tokens <= i.
+ *          [T] int64: new token i sees the earlier tokens and, of its
+ *          request's new tokens, those whose bit is set in tree_mask (bit j:
+ *          new token j; up to 64 new tokens a request, later ones are
+ *          hidden). Set the token's own bit to let it see itself. Infinities
+ *          and NaN in rows that a token does not see do not reach it.
+ * out      [T, n_heads, 128] rows out_ld apart; lse optional [T, n_heads]
+ *          fp32. A token that sees nothing gives out 0 and lse -inf.
+ * ws       moe_mla_decode_workspace(T, n_heads) bytes.
+ * Limits: B <= 65536, T * n_heads <= 2^24, page_size * n_pages and page_size
+ * * max_pages < 2^31, (T * n_heads / 32 + B) * page_size * max_pages / 64 <
+ * 2^30. B == 0 or T == 0 is a no-op.
+ */
+int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, const void* w_uv,
+                   int fmt, const void* cache, int page_size, int n_pages,
+                   const int32_t* page_table, int max_pages, const int32_t* lens,
+                   const int32_t* cu_q, const int64_t* tree_mask, int B, int T,
+                   int n_heads, float scale, void* out, int64_t out_ld, float* lse,
+                   void* ws, size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

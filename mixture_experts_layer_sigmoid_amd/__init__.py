@@ -5,7 +5,8 @@ permute, grouped fc1 + SwiGLU, grouped fc2, weighted combine, MX
 and NVFP4 quantization) runs in the hand-written HIP library libmoe_mi355x.so behind
 the C ABI of include/moe_mi355x.h. This package is its Python binding: the
 functions in `_lib` carry the C names and only marshal arguments; `layer`
-strings them into a forward pass. There is no CPU fallback: every binding call
+strings them into a forward pass, `mla` holds the latent attention beside it
+(expanded form with its backward, absorbed form over a paged cache). There is no CPU fallback: every binding call
 loads the built library and raises when it is missing.
 """
 from ._lib import (  # noqa: F401
@@ -20,7 +21,10 @@ from ._lib import (  # noqa: F401
     moe_grouped_mlp_bwd, moe_grouped_mlp_bwd_workspace, moe_route_bwd, moe_route_bwd_workspace,
     moe_bias_update, moe_nvfp4_tensor_scale, moe_quantize_nvfp4, moe_grouped_fc1_swiglu_nvfp4,
     moe_grouped_fc2_nvfp4,
+    moe_mla_attn_fwd, moe_mla_attn_bwd, moe_mla_attn_bwd_workspace, moe_mla_append, moe_mla_decode,
+    moe_mla_decode_workspace,
     SIGNATURES, LIB_PATH,
 )
 from .layer import (MoEForward, MoEBackward, RouterBackward, ExpertWeights, bias_update,  # noqa: F401
                     quantize_mx, quantize_mx_t, FMT)
+from .mla import LatentAttention, LatentDecode, latent_cache_append  # noqa: F401

@@ -57,6 +57,16 @@ SIGNATURES = {
     "moe_quantize_nvfp4": (_I, [_P, _I, _I64, _I, _I64, _P, _P, _P, _P, _P]),
     "moe_grouped_fc1_swiglu_nvfp4": (_I, [_P, _P, _P, _P, _P, _F, _F, _P, _I, _I, _I, _I64, _P, _P]),
     "moe_grouped_fc2_nvfp4": (_I, [_P, _P, _P, _P, _F, _P, _I, _I, _I, _I64, _P, _P]),
+    "moe_mla_attn_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I64,
+                              _P, _P]),
+    "moe_mla_attn_bwd_workspace": (_SZ, [_I, _I, _I]),
+    "moe_mla_attn_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _P, _I64, _P, _P, _P, _I, _I,
+                              _I, _I, _I, _F, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "moe_mla_append": (_I, [_P, _I64, _I, _P, _F, _P, _P, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _I64,
+                            _I, _I, _P]),
+    "moe_mla_decode_workspace": (_SZ, [_I, _I]),
+    "moe_mla_decode": (_I, [_P, _I64, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _I, _I, _I, _F, _P,
+                            _I64, _P, _P, _SZ, _P]),
     "moe_grouped_mlp_bwd_workspace": (_SZ, [_I, _I, _I, _I, _I, _I64, _I]),
     "moe_grouped_mlp_bwd": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                  _I, _I64, _P, _P, _P, _P, _SZ, _P]),
@@ -312,3 +322,44 @@ def moe_grouped_fc2_nvfp4(h_vals, w2, w2_scales, w2_g, h_g, offsets, E, H, F, ro
     _check("moe_grouped_fc2_nvfp4", load().moe_grouped_fc2_nvfp4(
         _ptr(h_vals), _ptr(w2), _ptr(w2_scales), _ptr(w2_g), h_g, _ptr(offsets), E, H, F, rows,
         _ptr(y), _stream(stream)))
+
+
+def moe_mla_attn_fwd(q, q_ld, kv, kv_ld, k_rope, kr_ld, fmt, cu_q, cu_k, B, Tq, Tk, n_heads, causal,
+                     scale, out, out_ld, lse, stream=None):
+    _check("moe_mla_attn_fwd", load().moe_mla_attn_fwd(
+        _ptr(q), q_ld, _ptr(kv), kv_ld, _ptr(k_rope), kr_ld, fmt, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk,
+        n_heads, causal, scale, _ptr(out), out_ld, _ptr(lse), _stream(stream)))
+
+
+def moe_mla_attn_bwd_workspace(Tq, Tk, n_heads) -> int:
+    return load().moe_mla_attn_bwd_workspace(Tq, Tk, n_heads)
+
+
+def moe_mla_attn_bwd(dout, dout_ld, q, q_ld, kv, kv_ld, k_rope, kr_ld, fmt, out, out_ld, lse, cu_q,
+                     cu_k, B, Tq, Tk, n_heads, causal, scale, dq, dq_ld, dkv, dkv_ld, dk_rope, dkr_ld,
+                     ws, stream=None):
+    _check("moe_mla_attn_bwd", load().moe_mla_attn_bwd(
+        _ptr(dout), dout_ld, _ptr(q), q_ld, _ptr(kv), kv_ld, _ptr(k_rope), kr_ld, fmt, _ptr(out),
+        out_ld, _ptr(lse), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, n_heads, causal, scale, _ptr(dq), dq_ld,
+        _ptr(dkv), dkv_ld, _ptr(dk_rope), dkr_ld, _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_mla_append(kv_a, kv_ld, fmt, norm_w, eps, cos, sin, max_pos, positions, interleaved, slots,
+                   cache, n_slots, q, q_ld, q_out, qo_ld, T, n_heads, stream=None):
+    _check("moe_mla_append", load().moe_mla_append(
+        _ptr(kv_a), kv_ld, fmt, _ptr(norm_w), eps, _ptr(cos), _ptr(sin), max_pos, _ptr(positions),
+        interleaved, _ptr(slots), _ptr(cache), n_slots, _ptr(q), q_ld, _ptr(q_out), qo_ld, T, n_heads,
+        _stream(stream)))
+
+
+def moe_mla_decode_workspace(T, n_heads) -> int:
+    return load().moe_mla_decode_workspace(T, n_heads)
+
+
+def moe_mla_decode(q, q_ld, w_uk, w_uv, fmt, cache, page_size, n_pages, page_table, max_pages, lens,
+                   cu_q, tree_mask, B, T, n_heads, scale, out, out_ld, lse, ws, stream=None):
+    _check("moe_mla_decode", load().moe_mla_decode(
+        _ptr(q), q_ld, _ptr(w_uk), _ptr(w_uv), fmt, _ptr(cache), page_size, n_pages, _ptr(page_table),
+        max_pages, _ptr(lens), _ptr(cu_q), _ptr(tree_mask), B, T, n_heads, scale, _ptr(out), out_ld,
+        _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))

@@ -1,0 +1,616 @@
+// moe_mla_decode: latent attention over a paged cache, in absorbed form.
+//
+// With q_lat[t, h] = W_UK[h]^T q[t, h, :128] every head's scores are taken
+// against the cached rows themselves:
+//   s[j] = scale * (q_lat . c_j + q[t, h, 128:] . kr_j),  p = softmax(s)
+//   o_lat = sum_j p_j c_j,   out[t, h] = W_UV[h] o_lat
+// One cached row (512 latent values, 64 rotary ones) serves all heads as key
+// and as value, so the heads of a request's new tokens are the rows of one
+// matrix product over its cache.
+//
+// Three launches: the products with W_UK; the attention, its work cut evenly
+// over the chip along the cached tokens; the joining of the pieces with the
+// products with W_UV.
+#include "mla.h"
+
+#include <cmath>
+
+namespace moe {
+namespace mla {
+namespace {
+
+constexpr int kTok = 64;                               // cached tokens per tile
+constexpr int kLat = kTok * kR * 2, kRope = kTok * kDr * 2, kTile = kLat + kRope;
+constexpr int kGroups = 256;                           // workgroups of the attention
+
+struct DecodeArgs {
+  const uint16_t* q;
+  int64_t q_ld;
+  const uint16_t* w_uk;      // [nh, 512, 128]
+  const uint16_t* w_uv;      // [nh, 128, 512]
+  const uint16_t* cache;
+  int page_size, n_pages;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* lens;
+  const int32_t* cu_q;
+  const uint64_t* tree;
+  int B, T, nh;
+  float scale;
+  uint16_t* out;
+  int64_t out_ld;
+  float* lse;
+  uint16_t* q_lat;           // [T * nh, 512]
+  float* o_full;             // [T * nh, 512]: rows whose cache one workgroup covered
+  float* part;               // [2 kGroups, rows, 512]: pieces, not normalized
+  float2* part_ml;           // [2 kGroups, rows]: their (maximum, sum)
+  int2* info;                // [T * nh]: (first piece, pieces), 0 pieces: in o_full
+  float* lse_full;           // [T * nh]
+};
+
+// ---- q_lat = q_nope . W_UK ---------------------------------------------------
+// A wave keeps 32 latent columns of one head's matrix (32 registers) and
+// takes the tokens in blocks of 32.
+constexpr int kAbsorbTok = 128;
+__global__ __launch_bounds__(256) void absorb_kernel(DecodeArgs p) {
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int h = blockIdx.y;
+  const int r0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 32;
+  const uint16_t* w = p.w_uk + (static_cast<int64_t>(h) * kR + r0 + (lane & 31)) * kDn + 8 * g;
+  bf16x8_t wf[8];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 16 * s);
+  const int t_end = min(p.T, (static_cast<int>(blockIdx.z) + 1) * kAbsorbTok);
+  for (int t0 = blockIdx.z * kAbsorbTok; t0 < t_end; t0 += 32) {
+    const int t = t0 + (lane & 31);
+    const uint16_t* q = p.q + static_cast<int64_t>(min(t, p.T - 1)) * p.q_ld + h * kDq + 8 * g;
+    f32x16_t a = f32x16_t{};
+#pragma unroll
+    for (int s = 0; s < 8; ++s) a = mfma(wf[s], *reinterpret_cast<const bf16x8_t*>(q + 16 * s), a);
+    if (t < t_end) {
+      uint16_t* o = p.q_lat + (static_cast<int64_t>(t) * p.nh + h) * kR + r0 + 4 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint2*>(o + 8 * i) = pack4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+    }
+  }
+}
+
+// ---- the work list -------------------------------------------------------------
+// Sequence b's new tokens and heads are n_q nh rows in ceil(n_q nh / rows)
+// row tiles; each row tile has to pass max(1, ceil(len / 64)) token tiles.
+// The (sequence, row tile, token tile) units in that order are cut into
+// equal runs, one for each workgroup.
+struct Seq {
+  int q0, nq, len, row_tiles, tok_tiles, units;
+};
+__device__ __forceinline__ Seq load_seq(const DecodeArgs& p, int b, int rows) {
+  Seq s{0, 0, 0, 0, 0, 0};
+  if (b < p.B) {
+    s.q0 = clamp_int(p.cu_q[b], 0, p.T);
+    s.nq = clamp_int(p.cu_q[b + 1], s.q0, p.T) - s.q0;
+    s.len = clamp_int(p.lens[b], 0, p.max_pages * p.page_size);
+    s.row_tiles = (s.nq * p.nh + rows - 1) / rows;
+    s.tok_tiles = s.len > 0 ? (s.len + kTok - 1) / kTok : 1;
+    s.units = s.row_tiles * s.tok_tiles;
+  }
+  return s;
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ int total_units(const DecodeArgs& p, int rows) {
+  int n = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 64)
+    n += __builtin_amdgcn_readlane(wave_scan(load_seq(p, b0 + (threadIdx.x & 63), rows).units), 63);
+  return n;
+}
+// sequence of unit u (u < total): its data and first unit
+__device__ __forceinline__ Seq find_unit(const DecodeArgs& p, int rows, int u, int& b_out, int& first) {
+  int before = 0;
+  Seq r{0, 0, 0, 0, 1, 0};
+  b_out = 0;
+  first = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 64) {
+    const Seq s = load_seq(p, b0 + (threadIdx.x & 63), rows);
+    const int sum = wave_scan(s.units);
+    const uint64_t hit = __ballot(before + sum > u);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      r.q0 = __builtin_amdgcn_readlane(s.q0, l);
+      r.nq = __builtin_amdgcn_readlane(s.nq, l);
+      r.len = __builtin_amdgcn_readlane(s.len, l);
+      r.row_tiles = __builtin_amdgcn_readlane(s.row_tiles, l);
+      r.tok_tiles = __builtin_amdgcn_readlane(s.tok_tiles, l);
+      r.units = __builtin_amdgcn_readlane(s.units, l);
+      b_out = b0 + l;
+      first = before + __builtin_amdgcn_readlane(sum, l) - r.units;
+      return r;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return r;
+}
+
+// zero the bf16 values of a 16-byte piece that are infinite or NaN
+__device__ __forceinline__ bool drop_nonfinite(u32x4_t& v) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((v[i] & 0x7F800000u) == 0x7F800000u) v[i] &= 0x0000FFFFu, bad = true;
+    if ((v[i] & 0x00007F80u) == 0x00007F80u) v[i] &= 0xFFFF0000u, bad = true;
+  }
+  return bad;
+}
+
+__device__ __forceinline__ void scale_operand(bf16x8_t& v, float f) {
+  typedef float f32x8_t __attribute__((ext_vector_type(8)));
+  v = __builtin_convertvector(__builtin_convertvector(v, f32x8_t) * f, bf16x8_t);
+}
+
+// The sums stay in the accumulation registers from the first product to the
+// last. Ordinary code that reads one (the rescaling, the final store) would
+// make the compiler keep them in vector registers between the products and
+// copy all 128 back and forth in every tile, so it reads them through
+// read_acc. The reads come long after the products that wrote the sums: the
+// scores of the same tile, products issued later, have already been used.
+__device__ __forceinline__ void keep_acc(f32x16_t& v) { asm volatile("" : "+a"(v)); }
+__device__ __forceinline__ float read_acc(float v) {
+  float r;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(r) : "a"(v));
+  return r;
+}
+
+// Workgroup: WR blocks of 32 rows x 2 waves. Wave (r, c) holds the queries of
+// row block r (144 registers) and the sums of latent columns 256 c .. (128
+// registers). Per token tile it scores the 32 tokens of half c, hands their
+// weights to its partner through LDS and multiplies all 64 tokens' weights
+// with its columns. (32 rows x all 512 columns per wave would need 400
+// registers for the kept operands alone, and spills.)
+// The two halves' weights refer to each wave's own running maximum; where
+// one grew, both are brought to the larger before the product.
+constexpr int kXchg = 64 * 32;                        // bytes of one wave's weights
+template <int WR>
+__global__ __launch_bounds__(128 * WR) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void decode_attn_kernel(DecodeArgs p) {
+  constexpr int NW = 2 * WR;
+  constexpr int kRows = 32 * WR;
+  constexpr int kRpw = kTok / NW;                     // token rows a wave loads
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kTile + NW * kXchg + NW * 128];
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+  uint8_t* xw = smem + 2 * kTile;
+  float* xref = reinterpret_cast<float*>(xw + NW * kXchg);
+
+  const int total = total_units(p, kRows);
+  const int per = (total + kGroups - 1) / kGroups;
+  const int grp = xcd_contiguous(blockIdx.x, kGroups);
+  int u = grp * per;
+  const int u_end = min(total, u + per);
+  const int u_begin = u;
+
+  uint32_t lat_off[8], rope_off[4], v_off[4][2];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) lat_off[s] = row_operand_offset<1024>(lane, s) + wc * 32 * 1024;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) rope_off[s] = kLat + row_operand_offset<128>(lane, s) + wc * 32 * 128;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v_off[c][h] = col_operand_offset<1024>(lane, c, h) + wc * 512;
+  const float c2 = p.scale * kLog2e;
+
+  while (u < u_end) {
+    int b, first;
+    const Seq sq = find_unit(p, kRows, u, b, first);
+    const int rt = (u - first) / sq.tok_tiles;
+    const int kt0 = (u - first) - rt * sq.tok_tiles;
+    const int kt1 = min(sq.tok_tiles, kt0 + (u_end - u));      // token tiles [kt0, kt1) of this row tile
+    const bool whole = kt0 == 0 && kt1 == sq.tok_tiles;
+
+    const int n_rows = sq.nq * p.nh;
+    const int row = rt * kRows + wr * 32 + (lane & 31);
+    const int rowc = min(row, n_rows - 1);
+    const int tok = rowc / p.nh;                                // new token of the row
+    const int64_t grow = static_cast<int64_t>(sq.q0) * p.nh + rowc;
+    const int prefix = sq.len - sq.nq;                          // cached tokens before the new ones
+
+    // slots of the wave's token rows, lane i: row wave * kRpw + i
+    auto lookup = [&](int kt) -> int {
+      const int pos = kt * kTok + wave * kRpw + (lane & (kRpw - 1));
+      int page = 0;
+      if (pos < sq.len) page = p.table[static_cast<int64_t>(b) * p.max_pages + pos / p.page_size];
+      return pos < sq.len ? clamp_int(page, 0, p.n_pages - 1) * p.page_size + pos % p.page_size : -1;
+    };
+    u32x4_t rope[kRpw / 8];
+    auto load = [&](int slot_l, uint8_t* buf) {
+#pragma unroll
+      for (int i = 0; i < kRpw; ++i) {
+        const int slot = __builtin_amdgcn_readlane(slot_l, i);
+        const int r = wave * kRpw + i;
+        const __amdgpu_buffer_rsrc_t rs =
+            buf_rsrc(p.cache + static_cast<int64_t>(slot < 0 ? 0 : slot) * kDc, slot < 0 ? 0u : kR * 2u);
+        lds_load16_buf(rs, (lane ^ tile_key<1024>(r)) << 4, 0, buf + r * 1024);
+      }
+#pragma unroll
+      for (int i = 0; i < kRpw / 8; ++i) {
+        const int slot = __shfl(slot_l, i * 8 + (lane >> 3), 64);
+        rope[i] = u32x4_t{0u, 0u, 0u, 0u};
+        if (slot >= 0)
+          rope[i] = *reinterpret_cast<const u32x4_t*>(p.cache + static_cast<int64_t>(slot) * kDc + kR + (lane & 7) * 8);
+      }
+    };
+    auto put_rope = [&](uint8_t* buf) {
+#pragma unroll
+      for (int i = 0; i < kRpw / 8; ++i) {
+        const int r = wave * kRpw + i * 8 + (lane >> 3);
+        *reinterpret_cast<u32x4_t*>(buf + kLat + r * 128 + (((lane & 7) ^ tile_key<128>(r)) << 4)) = rope[i];
+      }
+    };
+
+    const bool any = sq.len > 0;
+    int slot_next = -1;
+    if (any) {
+      load(lookup(kt0), smem);
+      if (kt0 + 1 < kt1) slot_next = lookup(kt0 + 1);
+    }
+    bf16x8_t qf[kDc / 16];
+    {
+      const uint16_t* ql = p.q_lat + grow * kR + 8 * g;
+      const uint16_t* qr = p.q + (static_cast<int64_t>(sq.q0) + tok) * p.q_ld + (rowc - tok * p.nh) * kDq + kDn + 8 * g;
+#pragma unroll
+      for (int s = 0; s < 32; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(ql + 16 * s);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) qf[32 + s] = *reinterpret_cast<const bf16x8_t*>(qr + 16 * s);
+    }
+    const uint64_t sees = p.tree ? p.tree[sq.q0 + tok] : 0u;
+    f32x16_t o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      o[c] = f32x16_t{};
+      keep_acc(o[c]);
+    }
+    float m = -INFINITY, l = 0.f;
+
+    for (int kt = kt0; any && kt < kt1; ++kt) {
+      uint8_t* buf = smem + ((kt - kt0) & 1) * kTile;
+      put_rope(buf);                  // the buffer's last readers are a barrier behind
+      wait_vmcnt<0>();
+      lds_barrier();
+      if (kt + 1 < kt1) {
+        load(slot_next, smem + ((kt + 1 - kt0) & 1) * kTile);
+        if (kt + 2 < kt1) slot_next = lookup(kt + 2);
+      }
+      const int t0 = kt * kTok;
+      f32x16_t s = f32x16_t{};
+#pragma unroll
+      for (int k = 0; k < 32; ++k) s = mfma(row_operand(buf, lat_off[k & 7] + (k >> 3) * 256), qf[k], s);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s = mfma(row_operand(buf, rope_off[k]), qf[32 + k], s);
+      const bool tail = t0 + kTok > prefix;
+      if (tail) {
+        // the tile holds new tokens (or the end of the cache): bit j of
+        // `hide` is place j of the tile
+        const int first_new = prefix - t0;                     // may lie outside [0, 64)
+        uint64_t hide;
+        if (p.tree) {
+          hide = first_new <= 0 ? ~uint64_t{0} : ~uint64_t{0} << first_new;
+          hide &= ~(first_new >= 0 ? sees << first_new : (first_new > -64 ? sees >> -first_new : 0u));
+        } else {
+          const int n_shown = first_new + tok + 1;             // places before this one are shown
+          hide = n_shown <= 0 ? ~uint64_t{0} : (n_shown < 64 ? ~uint64_t{0} << n_shown : 0u);
+        }
+        if (sq.len - t0 < kTok) hide |= ~uint64_t{0} << (sq.len - t0);
+        const uint32_t w = static_cast<uint32_t>(hide >> (32 * wc)) >> (4 * g);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = (w >> (8 * (i >> 2) + (i & 3))) & 1u ? -INFINITY : s[i];
+      }
+      float mx = s[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+      mx = fmaxf(mx, other_half(mx));
+      const float ref = fmaxf(m, mx);
+      // rows that have seen no key yet keep -inf: exponents against 0
+      const float rc = ref == -INFINITY ? 0.f : ref * c2;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = exp2_hw(fmaf(s[i], c2, -rc));
+        sum += s[i];
+      }
+      bf16x8_t pf[2][2];              // [half][k-step]
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<bf16x8_t*>(xw + wave * kXchg + k * 1024 + lane * 16) = pack_operand(s, k);
+      if (g == 0) xref[wave * 32 + lane] = ref;
+      lds_barrier();
+      if (tail && (p.tree || sq.nq > 1)) {
+        // a hidden token's row is still in the value product, with weight 0:
+        // values that are not finite must not reach it (rows that see the
+        // token have them in their scores already)
+        for (int i = threadIdx.x; i < kLat / 16; i += 64 * NW) {
+          u32x4_t v = *reinterpret_cast<const u32x4_t*>(buf + i * 16);
+          if (drop_nonfinite(v)) *reinterpret_cast<u32x4_t*>(buf + i * 16) = v;
+        }
+        lds_barrier();
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          pf[h][k] = *reinterpret_cast<const bf16x8_t*>(xw + (wave - wc + h) * kXchg + k * 1024 + lane * 16);
+      const float refp = xref[(wave ^ 1) * 32 + (lane & 31)];
+      const float mn = fmaxf(ref, refp);
+      if (__any(mn > m)) {
+        const float mc = mn == -INFINITY ? 0.f : mn * c2;
+        const float a = exp2_hw(fmaf(m, c2, -mc));
+        const float fo = exp2_hw(fmaf(ref, c2, -mc)), fp = exp2_hw(fmaf(refp, c2, -mc));
+        l *= a;
+        sum *= fo;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) scale_operand(pf[h][k], h == wc ? fo : fp);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[c][i] = read_acc(o[c][i]) * a;
+          keep_acc(o[c]);
+        }
+        m = mn;
+      }
+      l += sum;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          o[c] = mfma(col_operand(buf, v_off[c & 3][0] + (c >> 2) * 256 + k * 16 * 1024,
+                                  v_off[c & 3][1] + (c >> 2) * 256 + k * 16 * 1024),
+                      pf[k >> 1][k & 1], o[c]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) keep_acc(o[c]);
+    }
+    asm volatile("s_nop 15\n\ts_nop 15");   // the last product's result is in its registers
+    l += other_half(l);
+    lds_barrier();                    // everyone is done with the buffers
+    if (g == 0) xref[wave * 32 + lane] = l;
+    lds_barrier();
+    // in the same order in both waves
+    l = xref[(wave & ~1) * 32 + (lane & 31)] + xref[(wave | 1) * 32 + (lane & 31)];
+    lds_barrier();
+    if (row < n_rows) {
+      float* dst;
+      float f = 1.f;
+      const bool writer = wc == 0 && g == 0;
+      const int slot = 2 * grp + (u == u_begin ? 0 : 1);
+      if (whole) {
+        dst = p.o_full + grow * kR;
+        f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        if (writer) {
+          p.lse_full[grow] = l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
+          p.info[grow] = make_int2(0, 0);
+        }
+      } else {
+        const int64_t pr = static_cast<int64_t>(slot) * kRows + wr * 32 + (lane & 31);
+        dst = p.part + pr * kR;
+        if (writer) {
+          p.part_ml[pr] = make_float2(m, l);
+          if (kt0 == 0) {
+            // pieces of the row tile: this one and one of each following
+            // workgroup up to the one that holds the last token tile
+            const int last_unit = first + (rt + 1) * sq.tok_tiles - 1;
+            p.info[grow] = make_int2(slot, last_unit / per - grp + 1);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4_t*>(dst + 256 * wc + 32 * c + 8 * i + 4 * g) =
+              f32x4_t{read_acc(o[c][4 * i]) * f, read_acc(o[c][4 * i + 1]) * f, read_acc(o[c][4 * i + 2]) * f,
+                      read_acc(o[c][4 * i + 3]) * f};
+    }
+    u += kt1 - kt0;
+  }
+}
+
+// ---- join the pieces, out = W_UV . o_lat --------------------------------------
+// A workgroup takes one head of 32 tokens: each wave joins 8 tokens' rows
+// into LDS, as two bf16 terms (16 significant bits, so the product adds no
+// rounding of its own), then computes 32 of the 128 value columns.
+constexpr int kJoinTok = 32;
+__global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kJoinTok * kR * 2];
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.x, t0 = blockIdx.y * kJoinTok;
+  const int lo = clamp_int(p.cu_q[0], 0, p.T), hi = clamp_int(p.cu_q[p.B], lo, p.T);
+  const float c2 = p.scale * kLog2e;
+  const uint16_t* w = p.w_uv + (static_cast<int64_t>(h) * kDv + wave * 32 + (lane & 31)) * kR + 8 * g;
+  bf16x8_t wf[8];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 16 * s);
+
+  for (int i = 0; i < kJoinTok / 4; ++i) {
+    const int r = wave * (kJoinTok / 4) + i;
+    const int t = t0 + r;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (t >= lo && t < hi) {
+      const int64_t grow = static_cast<int64_t>(t) * p.nh + h;
+      const int2 info = p.info[grow];
+      const int n = __builtin_amdgcn_readfirstlane(clamp_int(info.y, 0, kGroups));
+      float lse;
+      if (n == 0) {
+        load8_f32(p.o_full + grow * kR + 8 * lane, v);
+        lse = p.lse_full[grow];
+      } else {
+        const int slot0 = clamp_int(__builtin_amdgcn_readfirstlane(info.x), 0, 2 * kGroups - 1);
+        // the row's place in its row tile: row tiles start at multiples of
+        // `rows` from its sequence's first row
+        int b_first = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 64) {
+          const int bb = min(b0 + lane, p.B - 1);
+          const uint64_t in = __ballot(p.cu_q[bb] <= t);
+          if (in) b_first = b0 + 63 - __builtin_clzll(in);
+        }
+        const int q0 = clamp_int(p.cu_q[min(b_first, p.B - 1)], 0, t);
+        const int lr = ((t - q0) * p.nh + h) % rows;
+        auto piece = [&](int j) -> int64_t {
+          const int s = j == 0 ? slot0 : min(2 * (slot0 / 2 + j), 2 * kGroups - 1);
+          return static_cast<int64_t>(s) * rows + lr;
+        };
+        float m = -INFINITY, l = 0.f;
+        for (int j = lane; j < n; j += 64) m = fmaxf(m, p.part_ml[piece(j)].x);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+        const float mc = m == -INFINITY ? 0.f : m * c2;
+        for (int j = 0; j < n; ++j) {
+          const int64_t pr = piece(j);
+          const float2 ml = p.part_ml[pr];
+          const float a = exp2_hw(fmaf(ml.x, c2, -mc));
+          float x[8];
+          load8_f32(p.part + pr * kR + 8 * lane, x);
+          l = fmaf(ml.y, a, l);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(x[e], a, v[e]);
+        }
+        const float f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= f;
+        lse = l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
+      }
+      if (p.lse && lane == 0) p.lse[grow] = lse;
+    }
+    typedef float f32x8_t __attribute__((ext_vector_type(8)));
+    const f32x8_t x = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+    const bf16x8_t a = __builtin_convertvector(x, bf16x8_t);
+    const bf16x8_t b = __builtin_convertvector(x - __builtin_convertvector(a, f32x8_t), bf16x8_t);
+    const uint32_t o = r * 1024 + ((lane ^ tile_key<1024>(r)) << 4);
+    *reinterpret_cast<bf16x8_t*>(smem + o) = a;
+    *reinterpret_cast<bf16x8_t*>(smem + kJoinTok * 1024 + o) = b;
+  }
+  __syncthreads();
+  f32x16_t acc = f32x16_t{};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint32_t o = row_operand_offset<1024>(lane, s) + q * 256;
+      acc = mfma(wf[s], row_operand(smem, o), acc);
+      acc = mfma(wf[s], row_operand(smem + kJoinTok * 1024, o), acc);
+    }
+    if (q < 3)
+#pragma unroll
+      for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 128 * (q + 1) + 16 * s);
+  }
+  const int t = t0 + (lane & 31);
+  if (t < lo || t >= hi) return;
+  uint16_t* o = p.out + static_cast<int64_t>(t) * p.out_ld + h * kDv + wave * 32 + 4 * g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint2*>(o + 8 * i) = pack4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+}
+
+// rows of a row tile: by the new rows a request brings on average
+int tile_rows(int64_t T, int B, int nh) {
+  const int64_t avg = (T * nh + B - 1) / B;
+  return avg <= 32 ? 32 : 64;
+}
+
+struct Layout {
+  size_t q_lat, o_full, part, part_ml, info, lse_full, total;
+};
+Layout layout(int64_t T, int nh) {
+  auto up = [](size_t v) { return (v + 255) & ~size_t{255}; };
+  const size_t n = static_cast<size_t>(T) * nh;
+  const size_t rows = n <= 32 ? 32 : 64;   // whatever B is
+  Layout l;
+  l.q_lat = 0;
+  l.o_full = up(n * kR * 2);
+  l.part = l.o_full + up(n * kR * 4);
+  l.part_ml = l.part + 2 * kGroups * rows * kR * 4;
+  l.info = l.part_ml + 2 * kGroups * rows * 8;
+  l.lse_full = l.info + up(n * 8);
+  l.total = l.lse_full + up(n * 4);
+  return l;
+}
+
+}  // namespace
+}  // namespace mla
+}  // namespace moe
+
+extern "C" size_t moe_mla_decode_workspace(int T, int n_heads) {
+  if (T < 0 || n_heads < 1 || n_heads > 1024 || static_cast<int64_t>(T) * n_heads > (1 << 24)) return 0;
+  return moe::mla::layout(T, n_heads).total;
+}
+
+extern "C" int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, const void* w_uv, int fmt,
+                              const void* cache, int page_size, int n_pages, const int32_t* page_table,
+                              int max_pages, const int32_t* lens, const int32_t* cu_q, const int64_t* tree_mask,
+                              int B, int T, int n_heads, float scale, void* out, int64_t out_ld, float* lse, void* ws,
+                              size_t ws_bytes, hipStream_t stream) {
+  using namespace moe;
+  using namespace moe::mla;
+  clear_error();
+  MOE_REQUIRE(B >= 0 && B <= (1 << 16) && T >= 0, MOE_ERR_INVALID_ARG,
+              "moe_mla_decode: need 0 <= B <= 65536 and T >= 0");
+  MOE_REQUIRE(n_heads >= 1 && n_heads <= 1024 && static_cast<int64_t>(T) * n_heads <= (1 << 24), MOE_ERR_INVALID_ARG,
+              "moe_mla_decode: n_heads must be in [1, 1024], T * n_heads <= 2^24");
+  MOE_REQUIRE(fmt == MOE_BF16, MOE_ERR_UNSUPPORTED, "moe_mla_decode: fmt must be MOE_BF16");
+  MOE_REQUIRE(page_size >= 1 && n_pages >= 1 && max_pages >= 1 &&
+                  static_cast<int64_t>(page_size) * n_pages < (int64_t{1} << 31) &&
+                  static_cast<int64_t>(page_size) * max_pages < (int64_t{1} << 31),
+              MOE_ERR_INVALID_ARG,
+              "moe_mla_decode: page_size, n_pages and max_pages must be >= 1, their products below 2^31");
+  MOE_REQUIRE(scale > 0.f && scale <= 3.0e38f, MOE_ERR_INVALID_ARG,
+              "moe_mla_decode: scale must be positive and finite");
+  MOE_REQUIRE(q_ld >= static_cast<int64_t>(n_heads) * kDq && out_ld >= static_cast<int64_t>(n_heads) * kDv &&
+                  q_ld <= kMaxLd && out_ld <= kMaxLd,
+              MOE_ERR_INVALID_ARG, "moe_mla_decode: a row stride is smaller than its row or above 2^23 elements");
+  MOE_REQUIRE(q_ld % 8 == 0 && out_ld % 8 == 0, MOE_ERR_ALIGNMENT,
+              "moe_mla_decode: row strides must be multiples of 8 elements");
+  if (B == 0 || T == 0) return MOE_OK;
+  const int rows = tile_rows(T, B, n_heads);
+  const int64_t tiles = static_cast<int64_t>(T) * n_heads / rows + B;
+  MOE_REQUIRE(tiles * ((static_cast<int64_t>(page_size) * max_pages + kTok - 1) / kTok) < (int64_t{1} << 30),
+              MOE_ERR_INVALID_ARG, "moe_mla_decode: too much work for one call (row tiles x cached tiles >= 2^30)");
+  MOE_REQUIRE(q && w_uk && w_uv && cache && page_table && lens && cu_q && out, MOE_ERR_INVALID_ARG,
+              "moe_mla_decode: null pointer");
+  MOE_REQUIRE(aligned16(q) && aligned16(w_uk) && aligned16(w_uv) && aligned16(cache) && aligned16(out) &&
+                  aligned16(ws),
+              MOE_ERR_ALIGNMENT, "moe_mla_decode: tensors and ws must be 16-byte aligned");
+  const Layout l = layout(T, n_heads);
+  MOE_REQUIRE(ws && ws_bytes >= l.total, MOE_ERR_WORKSPACE,
+              "moe_mla_decode: ws smaller than moe_mla_decode_workspace(T, n_heads)");
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  DecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(q), a.q_ld = q_ld;
+  a.w_uk = static_cast<const uint16_t*>(w_uk), a.w_uv = static_cast<const uint16_t*>(w_uv);
+  a.cache = static_cast<const uint16_t*>(cache);
+  a.page_size = page_size, a.n_pages = n_pages, a.table = page_table, a.max_pages = max_pages;
+  a.lens = lens, a.cu_q = cu_q, a.tree = reinterpret_cast<const uint64_t*>(tree_mask);
+  a.B = B, a.T = T, a.nh = n_heads, a.scale = scale;
+  a.out = static_cast<uint16_t*>(out), a.out_ld = out_ld, a.lse = lse;
+  a.q_lat = reinterpret_cast<uint16_t*>(w + l.q_lat);
+  a.o_full = reinterpret_cast<float*>(w + l.o_full);
+  a.part = reinterpret_cast<float*>(w + l.part);
+  a.part_ml = reinterpret_cast<float2*>(w + l.part_ml);
+  a.info = reinterpret_cast<int2*>(w + l.info);
+  a.lse_full = reinterpret_cast<float*>(w + l.lse_full);
+  hipLaunchKernelGGL(absorb_kernel, dim3(kR / 128, n_heads, (T + kAbsorbTok - 1) / kAbsorbTok), dim3(256), 0, stream,
+                     a);
+  if (rows == 32) hipLaunchKernelGGL(decode_attn_kernel<1>, dim3(kGroups), dim3(128), 0, stream, a);
+  else hipLaunchKernelGGL(decode_attn_kernel<2>, dim3(kGroups), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(decode_join_kernel, dim3(n_heads, (T + kJoinTok - 1) / kJoinTok), dim3(256), 0, stream, a, rows);
+  return check_launch("moe_mla_decode");
+}
