@@ -20,6 +20,8 @@
 
 #include "gemm_util.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace mla {
 
@@ -98,6 +100,17 @@ __device__ __forceinline__ bf16x8_t col_operand(const uint8_t* __restrict__ lds,
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// f(integral_constant<0>) ... f(integral_constant<N - 1>), unrolled at compile time
+template <int I, int N, typename Fn>
+__device__ __forceinline__ void static_for_impl(Fn&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for_impl<I + 1, N>(f);
+  }
+}
+template <int N, typename Fn>
+__device__ __forceinline__ void static_for(Fn&& f) { static_for_impl<0, N>(f); }
+
 __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -117,6 +130,16 @@ __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
+
+// Running reference of a row's weights 2^(x - ref): it follows the maximum
+// only once that has grown by more than 2^kLazy, so the sums are rescaled in
+// few tiles instead of nearly every one (with 32 rows a wave some row's
+// maximum grows almost always). Weights stay below 2^kLazy, far inside the
+// range of bf16 and fp32, whose precision does not depend on the scale.
+constexpr float kLazy = 8.f;
+__device__ __forceinline__ float next_ref(float ref, float mx, float c2) {
+  return (mx - ref) * c2 > kLazy ? mx : ref;       // ref -inf: taken whenever mx is finite
+}
 
 // value of the other half's lane (l ^ 32)
 __device__ __forceinline__ float other_half(float v) {

@@ -125,7 +125,7 @@ void attn_fwd_kernel(FwdArgs p) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
     mx = fmaxf(mx, other_half(mx));
-    const float mn = fmaxf(m, mx);
+    const float mn = next_ref(m, mx, c2);
     // a row that has seen no key yet keeps the maximum -inf: its exponents
     // are taken against 0, so every weight is 2^-inf = 0 and not NaN
     const float mc = mn == -INFINITY ? 0.f : mn * c2;

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kTok = 64;                               // cached tokens per tile
 constexpr int kLat = kTok * kR * 2, kRope = kTok * kDr * 2, kTile = kLat + kRope;
+constexpr int kAhead = 6;                              // matrix operands read ahead
 constexpr int kGroups = 256;                           // workgroups of the attention
 
 struct DecodeArgs {
@@ -30,12 +31,15 @@ struct DecodeArgs {
   const uint16_t* w_uv;      // [nh, 128, 512]
   const uint16_t* cache;
   int page_size, n_pages;
+  uint32_t page_magic;       // x / page_size = umulhi(2 x, page_magic) >> page_shift for 0 <= x < 2^31
+  int page_shift;
   const int32_t* table;
   int max_pages;
   const int32_t* lens;
   const int32_t* cu_q;
   const uint64_t* tree;
   int B, T, nh;
+  int team;                  // workgroups that take neighbouring row tiles together
   float scale;
   uint16_t* out;
   int64_t out_ld;
@@ -44,7 +48,7 @@ struct DecodeArgs {
   float* o_full;             // [T * nh, 512]: rows whose cache one workgroup covered
   float* part;               // [2 kGroups, rows, 512]: pieces, not normalized
   float2* part_ml;           // [2 kGroups, rows]: their (maximum, sum)
-  int2* info;                // [T * nh]: (first piece, pieces), 0 pieces: in o_full
+  int2* info;                // [T * nh]: (first piece, pieces + 2^16 row in the piece); 0 pieces: in o_full
   float* lse_full;           // [T * nh]
 };
 
@@ -79,20 +83,22 @@ __global__ __launch_bounds__(256) void absorb_kernel(DecodeArgs p) {
 // ---- the work list -------------------------------------------------------------
 // Sequence b's new tokens and heads are n_q nh rows in ceil(n_q nh / rows)
 // row tiles; each row tile has to pass max(1, ceil(len / 64)) token tiles.
-// The (sequence, row tile, token tile) units in that order are cut into
-// equal runs, one for each workgroup.
+// Neighbouring row tiles pass the same cached tokens, so `team` of them are
+// taken by as many workgroups of one XCD in step, and share its L2: the
+// (sequence, group of `team` row tiles, token tile) units in that order are
+// cut into equal runs, one for each team.
 struct Seq {
-  int q0, nq, len, row_tiles, tok_tiles, units;
+  int q0, nq, len, tok_tiles, units;
 };
 __device__ __forceinline__ Seq load_seq(const DecodeArgs& p, int b, int rows) {
-  Seq s{0, 0, 0, 0, 0, 0};
+  Seq s{0, 0, 0, 0, 0};
   if (b < p.B) {
     s.q0 = clamp_int(p.cu_q[b], 0, p.T);
     s.nq = clamp_int(p.cu_q[b + 1], s.q0, p.T) - s.q0;
     s.len = clamp_int(p.lens[b], 0, p.max_pages * p.page_size);
-    s.row_tiles = (s.nq * p.nh + rows - 1) / rows;
+    const int per = rows * p.team;
     s.tok_tiles = s.len > 0 ? (s.len + kTok - 1) / kTok : 1;
-    s.units = s.row_tiles * s.tok_tiles;
+    s.units = (s.nq * p.nh + per - 1) / per * s.tok_tiles;
   }
   return s;
 }
@@ -114,7 +120,7 @@ __device__ __forceinline__ int total_units(const DecodeArgs& p, int rows) {
 // sequence of unit u (u < total): its data and first unit
 __device__ __forceinline__ Seq find_unit(const DecodeArgs& p, int rows, int u, int& b_out, int& first) {
   int before = 0;
-  Seq r{0, 0, 0, 0, 1, 0};
+  Seq r{0, 0, 0, 1, 0};
   b_out = 0;
   first = 0;
   for (int b0 = 0; b0 < p.B; b0 += 64) {
@@ -126,7 +132,6 @@ __device__ __forceinline__ Seq find_unit(const DecodeArgs& p, int rows, int u, i
       r.q0 = __builtin_amdgcn_readlane(s.q0, l);
       r.nq = __builtin_amdgcn_readlane(s.nq, l);
       r.len = __builtin_amdgcn_readlane(s.len, l);
-      r.row_tiles = __builtin_amdgcn_readlane(s.row_tiles, l);
       r.tok_tiles = __builtin_amdgcn_readlane(s.tok_tiles, l);
       r.units = __builtin_amdgcn_readlane(s.units, l);
       b_out = b0 + l;
@@ -190,9 +195,11 @@ void decode_attn_kernel(DecodeArgs p) {
   float* xref = reinterpret_cast<float*>(xw + NW * kXchg);
 
   const int total = total_units(p, kRows);
-  const int per = (total + kGroups - 1) / kGroups;
+  const int teams = kGroups / p.team;
+  const int per = (total + teams - 1) / teams;
   const int grp = xcd_contiguous(blockIdx.x, kGroups);
-  int u = grp * per;
+  const int my_team = grp / p.team, member = grp % p.team;
+  int u = my_team * per;
   const int u_end = min(total, u + per);
   const int u_begin = u;
 
@@ -210,41 +217,54 @@ void decode_attn_kernel(DecodeArgs p) {
   while (u < u_end) {
     int b, first;
     const Seq sq = find_unit(p, kRows, u, b, first);
-    const int rt = (u - first) / sq.tok_tiles;
-    const int kt0 = (u - first) - rt * sq.tok_tiles;
+    const int rg = (u - first) / sq.tok_tiles;
+    const int kt0 = (u - first) - rg * sq.tok_tiles;
     const int kt1 = min(sq.tok_tiles, kt0 + (u_end - u));      // token tiles [kt0, kt1) of this row tile
     const bool whole = kt0 == 0 && kt1 == sq.tok_tiles;
+    const int rt = rg * p.team + member;
+    const int slot = 2 * grp + (u == u_begin ? 0 : 1);
+    u += kt1 - kt0;
 
     const int n_rows = sq.nq * p.nh;
+    if (rt * kRows >= n_rows) continue;                         // the last group has fewer row tiles
     const int row = rt * kRows + wr * 32 + (lane & 31);
     const int rowc = min(row, n_rows - 1);
     const int tok = rowc / p.nh;                                // new token of the row
     const int64_t grow = static_cast<int64_t>(sq.q0) * p.nh + rowc;
     const int prefix = sq.len - sq.nq;                          // cached tokens before the new ones
 
-    // slots of the wave's token rows, lane i: row wave * kRpw + i
-    auto lookup = [&](int kt) -> int {
-      const int pos = kt * kTok + wave * kRpw + (lane & (kRpw - 1));
-      int page = 0;
-      if (pos < sq.len) page = p.table[static_cast<int64_t>(b) * p.max_pages + pos / p.page_size];
-      return pos < sq.len ? clamp_int(page, 0, p.n_pages - 1) * p.page_size + pos % p.page_size : -1;
+    // Page and place of the wave's token rows, lane i: row wave * kRpw + i
+    // (rows past the cache's end repeat the last token's: their scores are
+    // masked and their values meet weight 0), and from them the row's byte
+    // address; apart, so that the page is waited for a tile later.
+    int page = 0, place = 0;
+    auto find_page = [&](int kt) {
+      const int pos = min(kt * kTok + wave * kRpw + (lane & (kRpw - 1)), sq.len - 1);
+      const int q = __umulhi(2 * static_cast<uint32_t>(pos), p.page_magic) >> p.page_shift;
+      place = pos - q * p.page_size;
+      page = p.table[static_cast<int64_t>(b) * p.max_pages + q];
+    };
+    auto row_address = [&]() -> uint64_t {
+      const int slot = clamp_int(page, 0, p.n_pages - 1) * p.page_size + place;
+      return reinterpret_cast<uint64_t>(p.cache) + static_cast<uint64_t>(slot) * (kDc * 2);
+    };
+    // row i of the wave's share into lds: 64 lanes x 16 bytes (zeros if
+    // `bytes` is 0)
+    auto load_row = [&](uint32_t bytes, uint64_t addr, uint8_t* lds, int i) {
+      const uint64_t a = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr), i)) & 0xFFFFFFFFu;
+      const uint64_t h = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr >> 32), i)) << 32;
+      const __amdgpu_buffer_rsrc_t rs = buf_rsrc(reinterpret_cast<const void*>(h | a), bytes);
+      lds_load16_buf(rs, (lane ^ tile_key<1024>(i)) << 4, 0, lds + i * 1024);   // kRpw % 16 == 0: key(row) = key(i)
     };
     u32x4_t rope[kRpw / 8];
-    auto load = [&](int slot_l, uint8_t* buf) {
-#pragma unroll
-      for (int i = 0; i < kRpw; ++i) {
-        const int slot = __builtin_amdgcn_readlane(slot_l, i);
-        const int r = wave * kRpw + i;
-        const __amdgpu_buffer_rsrc_t rs =
-            buf_rsrc(p.cache + static_cast<int64_t>(slot < 0 ? 0 : slot) * kDc, slot < 0 ? 0u : kR * 2u);
-        lds_load16_buf(rs, (lane ^ tile_key<1024>(r)) << 4, 0, buf + r * 1024);
-      }
+    auto load_rope = [&](uint64_t addr) {
+      typedef const __attribute__((address_space(1))) u32x4_t* gptr;
 #pragma unroll
       for (int i = 0; i < kRpw / 8; ++i) {
-        const int slot = __shfl(slot_l, i * 8 + (lane >> 3), 64);
-        rope[i] = u32x4_t{0u, 0u, 0u, 0u};
-        if (slot >= 0)
-          rope[i] = *reinterpret_cast<const u32x4_t*>(p.cache + static_cast<int64_t>(slot) * kDc + kR + (lane & 7) * 8);
+        const int lr = i * 8 + (lane >> 3);
+        const uint32_t a = __shfl(static_cast<int>(addr), lr, 64), h = __shfl(static_cast<int>(addr >> 32), lr, 64);
+        const uint64_t src = (static_cast<uint64_t>(h) << 32 | a) + kR * 2 + (lane & 7) * 16;
+        rope[i] = *reinterpret_cast<gptr>(src);
       }
     };
     auto put_rope = [&](uint8_t* buf) {
@@ -256,10 +276,14 @@ void decode_attn_kernel(DecodeArgs p) {
     };
 
     const bool any = sq.len > 0;
-    int slot_next = -1;
+    const int w_row = wave * kRpw;                              // first row of the wave's share
     if (any) {
-      load(lookup(kt0), smem);
-      if (kt0 + 1 < kt1) slot_next = lookup(kt0 + 1);
+      find_page(kt0);
+      const uint64_t a0 = row_address();
+      load_rope(a0);
+#pragma unroll
+      for (int i = 0; i < kRpw; ++i) load_row(kR * 2, a0, smem + w_row * 1024, i);
+      find_page(kt0 + 1);
     }
     bf16x8_t qf[kDc / 16];
     {
@@ -284,16 +308,34 @@ void decode_attn_kernel(DecodeArgs p) {
       put_rope(buf);                  // the buffer's last readers are a barrier behind
       wait_vmcnt<0>();
       lds_barrier();
-      if (kt + 1 < kt1) {
-        load(slot_next, smem + ((kt + 1 - kt0) & 1) * kTile);
-        if (kt + 2 < kt1) slot_next = lookup(kt + 2);
-      }
+      // the next tile's rows (zeros behind the last)
+      const uint32_t next_bytes = kt + 1 < kt1 ? kR * 2 : 0;
+      const uint64_t next_addr = row_address();
+      uint32_t next_ofs = ((kt + 1 - kt0) & 1) * kTile + w_row * 1024;
+      asm volatile("" : "+s"(next_ofs));                        // not one register per row
       const int t0 = kt * kTok;
+      // scores: operands read kAhead steps ahead; the next tile's rows are
+      // issued between the products
       f32x16_t s = f32x16_t{};
-#pragma unroll
-      for (int k = 0; k < 32; ++k) s = mfma(row_operand(buf, lat_off[k & 7] + (k >> 3) * 256), qf[k], s);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s = mfma(row_operand(buf, rope_off[k]), qf[32 + k], s);
+      {
+        bf16x8_t a[kAhead];
+        auto fetch = [&](auto k_c) {
+          constexpr int k = decltype(k_c)::value;
+          if constexpr (k < 32) a[k % kAhead] = row_operand(buf, lat_off[k & 7] + (k >> 3) * 256);
+          else a[k % kAhead] = row_operand(buf, rope_off[k - 32]);
+        };
+        static_for<kAhead>([&](auto k_c) { fetch(k_c); });
+        load_rope(next_addr);
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<36>([&](auto k_c) {
+          constexpr int k = decltype(k_c)::value;
+          s = mfma(a[k % kAhead], qf[k], s);
+          if constexpr (k + kAhead < 36) fetch(std::integral_constant<int, k + kAhead>{});
+          if constexpr (k < kRpw) load_row(next_bytes, next_addr, smem + next_ofs, k);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        find_page(kt + 2);
+      }
       const bool tail = t0 + kTok > prefix;
       if (tail) {
         // the tile holds new tokens (or the end of the cache): bit j of
@@ -316,7 +358,7 @@ void decode_attn_kernel(DecodeArgs p) {
 #pragma unroll
       for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
       mx = fmaxf(mx, other_half(mx));
-      const float ref = fmaxf(m, mx);
+      const float ref = next_ref(m, mx, c2);
       // rows that have seen no key yet keep -inf: exponents against 0
       const float rc = ref == -INFINITY ? 0.f : ref * c2;
       float sum = 0.f;
@@ -367,17 +409,27 @@ void decode_attn_kernel(DecodeArgs p) {
         m = mn;
       }
       l += sum;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          o[c] = mfma(col_operand(buf, v_off[c & 3][0] + (c >> 2) * 256 + k * 16 * 1024,
-                                  v_off[c & 3][1] + (c >> 2) * 256 + k * 16 * 1024),
-                      pf[k >> 1][k & 1], o[c]);
+      {
+        bf16x8_t a[kAhead];
+        auto fetch = [&](auto n_c) {
+          constexpr int n = decltype(n_c)::value, k = n / 8, c = n % 8;
+          a[n % kAhead] = col_operand(buf, v_off[c & 3][0] + (c >> 2) * 256 + k * 16 * 1024,
+                                      v_off[c & 3][1] + (c >> 2) * 256 + k * 16 * 1024);
+        };
+        static_for<kAhead>([&](auto n_c) { fetch(n_c); });
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<32>([&](auto n_c) {
+          constexpr int n = decltype(n_c)::value, k = n / 8, c = n % 8;
+          o[c] = mfma(a[n % kAhead], pf[k >> 1][k & 1], o[c]);
+          if constexpr (n + kAhead < 32) fetch(std::integral_constant<int, n + kAhead>{});
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) keep_acc(o[c]);
     }
     asm volatile("s_nop 15\n\ts_nop 15");   // the last product's result is in its registers
+    wait_vmcnt<0>();                  // the zeros behind the last tile have arrived
     l += other_half(l);
     lds_barrier();                    // everyone is done with the buffers
     if (g == 0) xref[wave * 32 + lane] = l;
@@ -389,7 +441,6 @@ void decode_attn_kernel(DecodeArgs p) {
       float* dst;
       float f = 1.f;
       const bool writer = wc == 0 && g == 0;
-      const int slot = 2 * grp + (u == u_begin ? 0 : 1);
       if (whole) {
         dst = p.o_full + grow * kR;
         f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -404,9 +455,9 @@ void decode_attn_kernel(DecodeArgs p) {
           p.part_ml[pr] = make_float2(m, l);
           if (kt0 == 0) {
             // pieces of the row tile: this one and one of each following
-            // workgroup up to the one that holds the last token tile
-            const int last_unit = first + (rt + 1) * sq.tok_tiles - 1;
-            p.info[grow] = make_int2(slot, last_unit / per - grp + 1);
+            // team up to the one that holds the last token tile
+            const int last_unit = first + (rg + 1) * sq.tok_tiles - 1;
+            p.info[grow] = make_int2(slot, (last_unit / per - my_team + 1) | (wr * 32 + lane) << 16);
           }
         }
       }
@@ -418,20 +469,24 @@ void decode_attn_kernel(DecodeArgs p) {
               f32x4_t{read_acc(o[c][4 * i]) * f, read_acc(o[c][4 * i + 1]) * f, read_acc(o[c][4 * i + 2]) * f,
                       read_acc(o[c][4 * i + 3]) * f};
     }
-    u += kt1 - kt0;
   }
 }
 
 // ---- join the pieces, out = W_UV . o_lat --------------------------------------
-// A workgroup takes one head of 32 tokens: each wave joins 8 tokens' rows
-// into LDS, as two bf16 terms (16 significant bits, so the product adds no
-// rounding of its own), then computes 32 of the 128 value columns.
+// A workgroup takes one head of up to 32 tokens (fewer when there are few, so
+// that the pieces' rows are read by enough workgroups): a wave joins a
+// token's pieces (several waves share them below 4 tokens), and puts the row
+// into LDS as two bf16 terms (16 significant bits, so the product adds no
+// rounding of its own); then each wave computes 32 of the 128 value columns.
 constexpr int kJoinTok = 32;
-__global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows) {
+constexpr int kJoinAhead = 4;          // pieces read at once
+__global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows, int toks) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kJoinTok * kR * 2];
+  __shared__ float sums[4][kR];
+  __shared__ float sums_l[4];
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.x, t0 = blockIdx.y * kJoinTok;
+  const int h = blockIdx.x, t0 = blockIdx.y * toks;
   const int lo = clamp_int(p.cu_q[0], 0, p.T), hi = clamp_int(p.cu_q[p.B], lo, p.T);
   const float c2 = p.scale * kLog2e;
   const uint16_t* w = p.w_uv + (static_cast<int64_t>(h) * kDv + wave * 32 + (lane & 31)) * kR + 8 * g;
@@ -439,67 +494,92 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows
 #pragma unroll
   for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 16 * s);
 
-  for (int i = 0; i < kJoinTok / 4; ++i) {
-    const int r = wave * (kJoinTok / 4) + i;
+  const int share = toks >= 4 ? 1 : 4 / toks;         // waves of one token
+  const int sub = wave % share;
+  for (int r = wave / share; r < toks; r += 4 / share) {
     const int t = t0 + r;
-    float v[8];
+    const bool in = t >= lo && t < hi;
+    const int64_t grow = static_cast<int64_t>(t) * p.nh + h;
+    int n = 0;
+    float m = -INFINITY, l = 0.f, v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (t >= lo && t < hi) {
-      const int64_t grow = static_cast<int64_t>(t) * p.nh + h;
+    if (in) {
       const int2 info = p.info[grow];
-      const int n = __builtin_amdgcn_readfirstlane(clamp_int(info.y, 0, kGroups));
-      float lse;
+      const int what = __builtin_amdgcn_readfirstlane(info.y);
+      n = clamp_int(what & 0xFFFF, 0, kGroups);
       if (n == 0) {
         load8_f32(p.o_full + grow * kR + 8 * lane, v);
-        lse = p.lse_full[grow];
       } else {
         const int slot0 = clamp_int(__builtin_amdgcn_readfirstlane(info.x), 0, 2 * kGroups - 1);
-        // the row's place in its row tile: row tiles start at multiples of
-        // `rows` from its sequence's first row
-        int b_first = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 64) {
-          const int bb = min(b0 + lane, p.B - 1);
-          const uint64_t in = __ballot(p.cu_q[bb] <= t);
-          if (in) b_first = b0 + 63 - __builtin_clzll(in);
-        }
-        const int q0 = clamp_int(p.cu_q[min(b_first, p.B - 1)], 0, t);
-        const int lr = ((t - q0) * p.nh + h) % rows;
+        const int lr = clamp_int(what >> 16, 0, rows - 1);
+        // the first piece may be its workgroup's second; the others are the
+        // first of the same member of the following teams
         auto piece = [&](int j) -> int64_t {
-          const int s = j == 0 ? slot0 : min(2 * (slot0 / 2 + j), 2 * kGroups - 1);
+          const int s = j == 0 ? slot0 : min(2 * (slot0 / 2 + j * p.team), 2 * kGroups - 1);
           return static_cast<int64_t>(s) * rows + lr;
         };
-        float m = -INFINITY, l = 0.f;
         for (int j = lane; j < n; j += 64) m = fmaxf(m, p.part_ml[piece(j)].x);
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
         const float mc = m == -INFINITY ? 0.f : m * c2;
-        for (int j = 0; j < n; ++j) {
-          const int64_t pr = piece(j);
-          const float2 ml = p.part_ml[pr];
-          const float a = exp2_hw(fmaf(ml.x, c2, -mc));
-          float x[8];
-          load8_f32(p.part + pr * kR + 8 * lane, x);
-          l = fmaf(ml.y, a, l);
+        for (int j = sub; j < n; j += kJoinAhead * share) {
+          float x[kJoinAhead][8];
+          float2 ml[kJoinAhead];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = fmaf(x[e], a, v[e]);
+          for (int q = 0; q < kJoinAhead; ++q) {
+            const int64_t pr = piece(min(j + q * share, n - 1));
+            ml[q] = p.part_ml[pr];
+            load8_f32(p.part + pr * kR + 8 * lane, x[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < kJoinAhead; ++q) {
+            if (j + q * share >= n) continue;
+            const float a = exp2_hw(fmaf(ml[q].x, c2, -mc));
+            l = fmaf(ml[q].y, a, l);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(x[q][e], a, v[e]);
+          }
         }
-        const float f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= f;
-        lse = l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
       }
-      if (p.lse && lane == 0) p.lse[grow] = lse;
     }
+    if (share > 1) {                  // the same for all waves: one token each or a share of it
+      store8_f32(&sums[wave][8 * lane], v);
+      if (lane == 0) sums_l[wave] = l;
+      __syncthreads();
+      const int w0 = wave - sub;
+      if (n > 0) {
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int q = 0; q < share; ++q) {
+          float x[8];
+          load8_f32(&sums[w0 + q][8 * lane], x);
+          l += sums_l[w0 + q];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += x[e];
+        }
+      }
+    }
+    if (n > 0) {
+      const float f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= f;
+    }
+    if (in && p.lse && lane == 0 && sub == 0)
+      p.lse[grow] = n == 0 ? p.lse_full[grow] : (l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2));
     typedef float f32x8_t __attribute__((ext_vector_type(8)));
     const f32x8_t x = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
     const bf16x8_t a = __builtin_convertvector(x, bf16x8_t);
     const bf16x8_t b = __builtin_convertvector(x - __builtin_convertvector(a, f32x8_t), bf16x8_t);
     const uint32_t o = r * 1024 + ((lane ^ tile_key<1024>(r)) << 4);
-    *reinterpret_cast<bf16x8_t*>(smem + o) = a;
-    *reinterpret_cast<bf16x8_t*>(smem + kJoinTok * 1024 + o) = b;
+    if (sub == 0) {
+      *reinterpret_cast<bf16x8_t*>(smem + o) = a;
+      *reinterpret_cast<bf16x8_t*>(smem + kJoinTok * 1024 + o) = b;
+    }
   }
   __syncthreads();
+  // columns at or past `toks` hold whatever LDS held and are not stored
   f32x16_t acc = f32x16_t{};
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -514,11 +594,28 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows
       for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 128 * (q + 1) + 16 * s);
   }
   const int t = t0 + (lane & 31);
-  if (t < lo || t >= hi) return;
+  if ((lane & 31) >= toks || t < lo || t >= hi) return;
   uint16_t* o = p.out + static_cast<int64_t>(t) * p.out_ld + h * kDv + wave * 32 + 4 * g;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     *reinterpret_cast<uint2*>(o + 8 * i) = pack4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+}
+
+// tokens of a joining workgroup: as many as leave two workgroups a compute unit
+int join_tokens(int T, int nh) {
+  int n = kJoinTok;
+  while (n > 1 && static_cast<int64_t>((T + n - 1) / n) * nh < 2 * kNumCu) n /= 2;
+  return n;
+}
+
+// Row tiles taken in step by as many workgroups: the largest power of two (at
+// most the 32 workgroups of an XCD) that leaves no more than a sixth of the
+// places empty for a request of average size.
+int team_size(int64_t T, int B, int nh, int rows) {
+  const int64_t tiles = ((T * nh + B - 1) / B + rows - 1) / rows;
+  int n = kGroups / kNumXcd;
+  while (n > 1 && (n > tiles || 6 * tiles < 5 * ((tiles + n - 1) / n * n))) n /= 2;
+  return n;
 }
 
 // rows of a row tile: by the new rows a request brings on average
@@ -598,6 +695,10 @@ extern "C" int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, con
   a.w_uk = static_cast<const uint16_t*>(w_uk), a.w_uv = static_cast<const uint16_t*>(w_uv);
   a.cache = static_cast<const uint16_t*>(cache);
   a.page_size = page_size, a.n_pages = n_pages, a.table = page_table, a.max_pages = max_pages;
+  int shift = 0;
+  while ((int64_t{1} << shift) < page_size) ++shift;
+  a.page_shift = shift;
+  a.page_magic = static_cast<uint32_t>(((uint64_t{1} << (31 + shift)) + page_size - 1) / page_size);
   a.lens = lens, a.cu_q = cu_q, a.tree = reinterpret_cast<const uint64_t*>(tree_mask);
   a.B = B, a.T = T, a.nh = n_heads, a.scale = scale;
   a.out = static_cast<uint16_t*>(out), a.out_ld = out_ld, a.lse = lse;
@@ -607,10 +708,13 @@ extern "C" int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, con
   a.part_ml = reinterpret_cast<float2*>(w + l.part_ml);
   a.info = reinterpret_cast<int2*>(w + l.info);
   a.lse_full = reinterpret_cast<float*>(w + l.lse_full);
+  a.team = team_size(T, B, n_heads, rows);
+  const int toks = join_tokens(T, n_heads);
   hipLaunchKernelGGL(absorb_kernel, dim3(kR / 128, n_heads, (T + kAbsorbTok - 1) / kAbsorbTok), dim3(256), 0, stream,
                      a);
   if (rows == 32) hipLaunchKernelGGL(decode_attn_kernel<1>, dim3(kGroups), dim3(128), 0, stream, a);
   else hipLaunchKernelGGL(decode_attn_kernel<2>, dim3(kGroups), dim3(256), 0, stream, a);
-  hipLaunchKernelGGL(decode_join_kernel, dim3(n_heads, (T + kJoinTok - 1) / kJoinTok), dim3(256), 0, stream, a, rows);
+  hipLaunchKernelGGL(decode_join_kernel, dim3(n_heads, (T + toks - 1) / toks), dim3(256), 0, stream, a, rows,
+                     toks);
   return check_launch("moe_mla_decode");
 }
