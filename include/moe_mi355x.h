@@ -755,8 +755,9 @@ size_t moe_mla_decode_workspace(int T, int n_heads);
  * rounding (q_lat is rounded to bf16 as matrix operand).
  * q        [T, n_heads, 192] rows q_ld apart: the new tokens of all requests,
  *          request b's are rows [cu_q[b], cu_q[b + 1]) (cu_q [B + 1] int32).
- * w_uk     [n_heads, 512, 128] bf16: each W_UK[h] transposed (laid out once);
- * w_uv     [n_heads, 128, 512] bf16.
+ * w_uk     [n_heads, 512, 128] bf16 (each W_UK[h] transposed) and
+ * w_uv     [n_heads, 128, 512] bf16, both packed once by moe_pack_weights
+ *          (MOE_BF16, E = n_heads, half = 0).
  * cache    [n_pages, page_size, 576] bf16 (moe_mla_append's rows), any
  *          page_size; page_table [B, max_pages] int32: request b's token j is
  *          place j % page_size of page page_table[b, j / page_size] (page ids

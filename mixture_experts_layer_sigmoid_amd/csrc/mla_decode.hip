@@ -27,8 +27,8 @@ constexpr int kGroups = 256;                           // workgroups of the atte
 struct DecodeArgs {
   const uint16_t* q;
   int64_t q_ld;
-  const uint16_t* w_uk;      // [nh, 512, 128]
-  const uint16_t* w_uv;      // [nh, 128, 512]
+  const uint16_t* w_uk;      // [nh, 512, 128] and [nh, 128, 512] in moe_pack_weights'
+  const uint16_t* w_uv;      // order: per 32 rows and 16 columns one 1 KB operand
   const uint16_t* cache;
   int page_size, n_pages;
   uint32_t page_magic;       // x / page_size = umulhi(2 x, page_magic) >> page_shift for 0 <= x < 2^31
@@ -45,37 +45,59 @@ struct DecodeArgs {
   int64_t out_ld;
   float* lse;
   uint16_t* q_lat;           // [T * nh, 512]
-  float* o_full;             // [T * nh, 512]: rows whose cache one workgroup covered
+  float* o_full;             // [T * nh, 512]: rows whose cache one workgroup covered, not normalized
   float* part;               // [2 kGroups, rows, 512]: pieces, not normalized
   float2* part_ml;           // [2 kGroups, rows]: their (maximum, sum)
-  int2* info;                // [T * nh]: (first piece, pieces + 2^16 row in the piece); 0 pieces: in o_full
-  float* lse_full;           // [T * nh]
+  int2* info;                // [T * nh]: (first piece, pieces + 2^16 row in the piece); 0 pieces: in o_full;
+                             // -1: a row that no request holds
+  float2* full_ml;           // [T * nh]: (maximum, sum) of o_full's rows
 };
 
 // ---- q_lat = q_nope . W_UK ---------------------------------------------------
 // A wave keeps 32 latent columns of one head's matrix (32 registers) and
-// takes the tokens in blocks of 32.
+// takes the tokens in blocks of 32. The results go through LDS, so that a
+// token's 128 columns leave as 256 consecutive bytes.
 constexpr int kAbsorbTok = 128;
+constexpr int kAbsorbRow = 256 + 16;                   // padded: rows 16 bytes apart in the banks
 __global__ __launch_bounds__(256) void absorb_kernel(DecodeArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2][32 * kAbsorbRow];
   const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int wave = threadIdx.x >> 6;
   const int h = blockIdx.y;
-  const int r0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 32;
-  const uint16_t* w = p.w_uk + (static_cast<int64_t>(h) * kR + r0 + (lane & 31)) * kDn + 8 * g;
-  bf16x8_t wf[8];
+  const int r0 = blockIdx.x * 128;
+  const uint16_t* w = p.w_uk + (static_cast<int64_t>(h) * kR + r0 + wave * 32) * kDn + lane * 8;
+  bf16x8_t wf[8], qf[8];
 #pragma unroll
-  for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 16 * s);
+  for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 512 * s);
   const int t_end = min(p.T, (static_cast<int>(blockIdx.z) + 1) * kAbsorbTok);
-  for (int t0 = blockIdx.z * kAbsorbTok; t0 < t_end; t0 += 32) {
-    const int t = t0 + (lane & 31);
-    const uint16_t* q = p.q + static_cast<int64_t>(min(t, p.T - 1)) * p.q_ld + h * kDq + 8 * g;
+  auto load_q = [&](int t0) {
+    const uint16_t* q = p.q + static_cast<int64_t>(min(t0 + (lane & 31), t_end - 1)) * p.q_ld + h * kDq + 8 * g;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(q + 16 * s);
+  };
+  const int t_begin = blockIdx.z * kAbsorbTok;
+  load_q(t_begin);
+  // rows that no request holds stay marked
+  if (blockIdx.x == 0)
+    for (int t = t_begin + threadIdx.x; t < t_end; t += 256)
+      p.info[static_cast<int64_t>(t) * p.nh + h] = make_int2(0, -1);
+  int cur = 0;
+  for (int t0 = t_begin; t0 < t_end; t0 += 32, cur ^= 1) {
     f32x16_t a = f32x16_t{};
 #pragma unroll
-    for (int s = 0; s < 8; ++s) a = mfma(wf[s], *reinterpret_cast<const bf16x8_t*>(q + 16 * s), a);
-    if (t < t_end) {
-      uint16_t* o = p.q_lat + (static_cast<int64_t>(t) * p.nh + h) * kR + r0 + 4 * g;
+    for (int s = 0; s < 8; ++s) a = mfma(wf[s], qf[s], a);
+    if (t0 + 32 < t_end) load_q(t0 + 32);
+    uint8_t* row = smem[cur] + (lane & 31) * kAbsorbRow + wave * 64 + 8 * g;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint2*>(o + 8 * i) = pack4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint2*>(row + 16 * i) = pack4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+    __syncthreads();                  // the other buffer's readers are a barrier behind
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 16 + (threadIdx.x >> 4), c = threadIdx.x & 15;
+      if (t0 + r < t_end)
+        *reinterpret_cast<u32x4_t*>(p.q_lat + (static_cast<int64_t>(t0 + r) * p.nh + h) * kR + r0 + 8 * c) =
+            *reinterpret_cast<const u32x4_t*>(smem[cur] + r * kAbsorbRow + 16 * c);
     }
   }
 }
@@ -111,34 +133,45 @@ __device__ __forceinline__ int wave_scan(int v) {
   }
   return v;
 }
-__device__ __forceinline__ int total_units(const DecodeArgs& p, int rows) {
-  int n = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64)
-    n += __builtin_amdgcn_readlane(wave_scan(load_seq(p, b0 + (threadIdx.x & 63), rows).units), 63);
+// The lanes hold 64 sequences; up to 64 sequences are loaded once.
+struct SeqBlock {
+  Seq s;
+  int sum;         // units up to and with this lane's sequence, within the block
+};
+__device__ __forceinline__ SeqBlock load_block(const DecodeArgs& p, int b0, int rows) {
+  SeqBlock k;
+  k.s = load_seq(p, b0 + (threadIdx.x & 63), rows);
+  k.sum = wave_scan(k.s.units);
+  return k;
+}
+__device__ __forceinline__ int total_units(const DecodeArgs& p, int rows, const SeqBlock& k0) {
+  int n = __builtin_amdgcn_readlane(k0.sum, 63);
+  for (int b0 = 64; b0 < p.B; b0 += 64) n += __builtin_amdgcn_readlane(load_block(p, b0, rows).sum, 63);
   return n;
 }
 // sequence of unit u (u < total): its data and first unit
-__device__ __forceinline__ Seq find_unit(const DecodeArgs& p, int rows, int u, int& b_out, int& first) {
+__device__ __forceinline__ Seq find_unit(const DecodeArgs& p, int rows, const SeqBlock& k0, int u, int& b_out,
+                                         int& first) {
   int before = 0;
   Seq r{0, 0, 0, 1, 0};
   b_out = 0;
   first = 0;
+  SeqBlock k = k0;
   for (int b0 = 0; b0 < p.B; b0 += 64) {
-    const Seq s = load_seq(p, b0 + (threadIdx.x & 63), rows);
-    const int sum = wave_scan(s.units);
-    const uint64_t hit = __ballot(before + sum > u);
+    if (b0 > 0) k = load_block(p, b0, rows);
+    const uint64_t hit = __ballot(before + k.sum > u);
     if (hit) {
       const int l = __builtin_ctzll(hit);
-      r.q0 = __builtin_amdgcn_readlane(s.q0, l);
-      r.nq = __builtin_amdgcn_readlane(s.nq, l);
-      r.len = __builtin_amdgcn_readlane(s.len, l);
-      r.tok_tiles = __builtin_amdgcn_readlane(s.tok_tiles, l);
-      r.units = __builtin_amdgcn_readlane(s.units, l);
+      r.q0 = __builtin_amdgcn_readlane(k.s.q0, l);
+      r.nq = __builtin_amdgcn_readlane(k.s.nq, l);
+      r.len = __builtin_amdgcn_readlane(k.s.len, l);
+      r.tok_tiles = __builtin_amdgcn_readlane(k.s.tok_tiles, l);
+      r.units = __builtin_amdgcn_readlane(k.s.units, l);
       b_out = b0 + l;
-      first = before + __builtin_amdgcn_readlane(sum, l) - r.units;
+      first = before + __builtin_amdgcn_readlane(k.sum, l) - r.units;
       return r;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
+    before += __builtin_amdgcn_readlane(k.sum, 63);
   }
   return r;
 }
@@ -194,7 +227,8 @@ void decode_attn_kernel(DecodeArgs p) {
   uint8_t* xw = smem + 2 * kTile;
   float* xref = reinterpret_cast<float*>(xw + NW * kXchg);
 
-  const int total = total_units(p, kRows);
+  const SeqBlock seqs = load_block(p, 0, kRows);
+  const int total = total_units(p, kRows, seqs);
   const int teams = kGroups / p.team;
   const int per = (total + teams - 1) / teams;
   const int grp = xcd_contiguous(blockIdx.x, kGroups);
@@ -216,7 +250,7 @@ void decode_attn_kernel(DecodeArgs p) {
 
   while (u < u_end) {
     int b, first;
-    const Seq sq = find_unit(p, kRows, u, b, first);
+    const Seq sq = find_unit(p, kRows, seqs, u, b, first);
     const int rg = (u - first) / sq.tok_tiles;
     const int kt0 = (u - first) - rg * sq.tok_tiles;
     const int kt1 = min(sq.tok_tiles, kt0 + (u_end - u));      // token tiles [kt0, kt1) of this row tile
@@ -438,27 +472,17 @@ void decode_attn_kernel(DecodeArgs p) {
     l = xref[(wave & ~1) * 32 + (lane & 31)] + xref[(wave | 1) * 32 + (lane & 31)];
     lds_barrier();
     if (row < n_rows) {
-      float* dst;
-      float f = 1.f;
       const bool writer = wc == 0 && g == 0;
-      if (whole) {
-        dst = p.o_full + grow * kR;
-        f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        if (writer) {
-          p.lse_full[grow] = l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
-          p.info[grow] = make_int2(0, 0);
-        }
-      } else {
-        const int64_t pr = static_cast<int64_t>(slot) * kRows + wr * 32 + (lane & 31);
-        dst = p.part + pr * kR;
-        if (writer) {
-          p.part_ml[pr] = make_float2(m, l);
-          if (kt0 == 0) {
-            // pieces of the row tile: this one and one of each following
-            // team up to the one that holds the last token tile
-            const int last_unit = first + (rg + 1) * sq.tok_tiles - 1;
-            p.info[grow] = make_int2(slot, (last_unit / per - my_team + 1) | (wr * 32 + lane) << 16);
-          }
+      const int64_t pr = static_cast<int64_t>(slot) * kRows + wr * 32 + (lane & 31);
+      float* dst = whole ? p.o_full + grow * kR : p.part + pr * kR;
+      if (writer) {
+        *(whole ? p.full_ml + grow : p.part_ml + pr) = make_float2(m, l);
+        if (kt0 == 0) {
+          // pieces of the row tile: this one and one of each following team
+          // up to the one that holds the last token tile
+          const int last_unit = first + (rg + 1) * sq.tok_tiles - 1;
+          const int n = whole ? 0 : last_unit / per - my_team + 1;
+          p.info[grow] = make_int2(slot, n | (wr * 32 + lane) << 16);
         }
       }
 #pragma unroll
@@ -466,141 +490,185 @@ void decode_attn_kernel(DecodeArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<f32x4_t*>(dst + 256 * wc + 32 * c + 8 * i + 4 * g) =
-              f32x4_t{read_acc(o[c][4 * i]) * f, read_acc(o[c][4 * i + 1]) * f, read_acc(o[c][4 * i + 2]) * f,
-                      read_acc(o[c][4 * i + 3]) * f};
+              f32x4_t{read_acc(o[c][4 * i]), read_acc(o[c][4 * i + 1]), read_acc(o[c][4 * i + 2]),
+                      read_acc(o[c][4 * i + 3])};
     }
   }
 }
 
 // ---- join the pieces, out = W_UV . o_lat --------------------------------------
-// A workgroup takes one head of up to 32 tokens (fewer when there are few, so
-// that the pieces' rows are read by enough workgroups): a wave joins a
-// token's pieces (several waves share them below 4 tokens), and puts the row
-// into LDS as two bf16 terms (16 significant bits, so the product adds no
-// rounding of its own); then each wave computes 32 of the 128 value columns.
-constexpr int kJoinTok = 32;
-constexpr int kJoinAhead = 4;          // pieces read at once
+// A workgroup takes one head of `toks` tokens (up to 32; fewer when there are
+// few, so that the pieces' rows are read by enough workgroups). A wave joins
+// the pieces of TPW tokens side by side (below 4 tokens several waves share
+// one token's pieces), and puts the rows into LDS as two bf16 terms (16
+// significant bits, so the product adds no rounding of its own); then each
+// wave computes 32 of the 128 value columns.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+template <int TPW>
 __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows, int toks) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kJoinTok * kR * 2];
-  __shared__ float sums[4][kR];
-  __shared__ float sums_l[4];
+  constexpr int kTokMax = 4 * TPW;
+  constexpr int kUnroll = TPW >= 4 ? 1 : 4 / TPW;      // pieces of a token read at once
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kTokMax * kR * 2];
+  __shared__ float sums[TPW == 1 ? 4 : 1][kR];
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = blockIdx.x, t0 = blockIdx.y * toks;
-  const int lo = clamp_int(p.cu_q[0], 0, p.T), hi = clamp_int(p.cu_q[p.B], lo, p.T);
   const float c2 = p.scale * kLog2e;
-  const uint16_t* w = p.w_uv + (static_cast<int64_t>(h) * kDv + wave * 32 + (lane & 31)) * kR + 8 * g;
-  bf16x8_t wf[8];
-#pragma unroll
-  for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 16 * s);
-
-  const int share = toks >= 4 ? 1 : 4 / toks;         // waves of one token
+  const int share = toks >= 4 ? 1 : 4 / toks;          // waves of one token
   const int sub = wave % share;
-  for (int r = wave / share; r < toks; r += 4 / share) {
-    const int t = t0 + r;
-    const bool in = t >= lo && t < hi;
-    const int64_t grow = static_cast<int64_t>(t) * p.nh + h;
-    int n = 0;
-    float m = -INFINITY, l = 0.f, v[8];
+
+  // What does not depend on another load is asked for at once: the rows'
+  // pieces (info), and their whole rows in case that is what they have (else
+  // what o_full holds there is not used). Token i of the wave is row
+  // wave / share + 4 i.
+  int64_t grow[TPW];
+  float v[TPW][8], m[TPW], l[TPW];
+  float2 ml[TPW];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (in) {
-      const int2 info = p.info[grow];
-      const int what = __builtin_amdgcn_readfirstlane(info.y);
-      n = clamp_int(what & 0xFFFF, 0, kGroups);
-      if (n == 0) {
-        load8_f32(p.o_full + grow * kR + 8 * lane, v);
-      } else {
-        const int slot0 = clamp_int(__builtin_amdgcn_readfirstlane(info.x), 0, 2 * kGroups - 1);
-        const int lr = clamp_int(what >> 16, 0, rows - 1);
-        // the first piece may be its workgroup's second; the others are the
-        // first of the same member of the following teams
-        auto piece = [&](int j) -> int64_t {
-          const int s = j == 0 ? slot0 : min(2 * (slot0 / 2 + j * p.team), 2 * kGroups - 1);
-          return static_cast<int64_t>(s) * rows + lr;
-        };
-        for (int j = lane; j < n; j += 64) m = fmaxf(m, p.part_ml[piece(j)].x);
+  for (int i = 0; i < TPW; ++i)
+    grow[i] = static_cast<int64_t>(min(t0 + wave / share + 4 * i, p.T - 1)) * p.nh + h;
+  const int2 info = p.info[static_cast<int64_t>(min(t0 + wave / share + 4 * (lane & (TPW - 1)), p.T - 1)) * p.nh + h];
 #pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-        const float mc = m == -INFINITY ? 0.f : m * c2;
-        for (int j = sub; j < n; j += kJoinAhead * share) {
-          float x[kJoinAhead][8];
-          float2 ml[kJoinAhead];
+  for (int i = 0; i < TPW; ++i) {
+    ml[i] = p.full_ml[grow[i]];
+    load8_f32(p.o_full + grow[i] * kR + 8 * lane, v[i]);
+  }
+  int n[TPW], slot0[TPW], lr[TPW];
+  bool held[TPW];
+  int n_max = 0;
 #pragma unroll
-          for (int q = 0; q < kJoinAhead; ++q) {
-            const int64_t pr = piece(min(j + q * share, n - 1));
-            ml[q] = p.part_ml[pr];
-            load8_f32(p.part + pr * kR + 8 * lane, x[q]);
-          }
+  for (int i = 0; i < TPW; ++i) {
+    const int y = __builtin_amdgcn_readlane(info.y, i);
+    held[i] = y >= 0 && t0 + wave / share + 4 * i < min(t0 + toks, p.T);
+    slot0[i] = clamp_int(__builtin_amdgcn_readlane(info.x, i), 0, 2 * kGroups - 1);
+    n[i] = held[i] ? clamp_int(y & 0xFFFF, 0, kGroups) : 0;
+    lr[i] = clamp_int(y >> 16, 0, rows - 1);
+    n_max = max(n_max, n[i]);
+  }
+
+  // row of a piece in part / part_ml: the first piece may be its workgroup's
+  // second, the others are the first of the same member of the teams after it
+  auto piece = [&](int i, int j) -> int64_t {
+    const int s = j == 0 ? slot0[i] : min(2 * (slot0[i] / 2 + j * p.team), 2 * kGroups - 1);
+    return static_cast<int64_t>(s) * rows + lr[i];
+  };
+  auto load_ml = [&](int i, int j) {
+    return j < n[i] ? p.part_ml[piece(i, j)] : make_float2(-INFINITY, 0.f);
+  };
 #pragma unroll
-          for (int q = 0; q < kJoinAhead; ++q) {
-            if (j + q * share >= n) continue;
-            const float a = exp2_hw(fmaf(ml[q].x, c2, -mc));
-            l = fmaf(ml[q].y, a, l);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(x[q][e], a, v[e]);
-          }
-        }
-      }
+  for (int i = 0; i < TPW; ++i) {
+    if (n[i] > 0) {
+      ml[i] = load_ml(i, lane);
+      m[i] = ml[i].x;
+      for (int j = 64 + lane; j < n[i]; j += 64) m[i] = fmaxf(m[i], load_ml(i, j).x);
+      m[i] = wave_max(m[i]);
+      l[i] = 0.f;
+    } else {
+      m[i] = ml[i].x;
+      l[i] = ml[i].y;
     }
-    if (share > 1) {                  // the same for all waves: one token each or a share of it
-      store8_f32(&sums[wave][8 * lane], v);
-      if (lane == 0) sums_l[wave] = l;
+    // a whole row counts once where several waves share a token
+    const bool keep = n[i] == 0 && sub == 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = keep ? v[i][e] : 0.f;
+  }
+  for (int c0 = 0; c0 < n_max; c0 += 64) {
+    float a[TPW];                                      // weight of piece c0 + lane
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      if (n[i] == 0) continue;
+      if (c0 > 0) ml[i] = load_ml(i, c0 + lane);
+      a[i] = exp2_hw(fmaf(ml[i].x, c2, m[i] == -INFINITY ? 0.f : -m[i] * c2));
+      l[i] += wave_sum(ml[i].y * a[i]);
+    }
+    const int c_end = min(64, n_max - c0);
+    for (int j = sub; j < c_end; j += kUnroll * share) {
+      float x[kUnroll][TPW][8];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < TPW; ++i) {
+          const int k = j + u * share;
+          if (k < c_end && c0 + k < n[i]) load8_f32(p.part + piece(i, c0 + k) * kR + 8 * lane, x[u][i]);
+        }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < TPW; ++i) {
+          const int k = j + u * share;
+          if (k >= c_end || c0 + k >= n[i]) continue;
+          const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a[i]), k));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] = fmaf(x[u][i][e], f, v[i][e]);
+        }
+    }
+  }
+  // the matrix, behind the pieces (loads return in order)
+  constexpr int kW = TPW <= 4 ? 32 : 16;
+  const uint16_t* w = p.w_uv + (static_cast<int64_t>(h) * kDv + wave * 32) * kR + lane * 8;
+  bf16x8_t wf[kW];
+#pragma unroll
+  for (int s = 0; s < kW; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 512 * s);
+  if constexpr (TPW == 1) {
+    if (share > 1) {
+      store8_f32(&sums[wave][8 * lane], v[0]);
       __syncthreads();
-      const int w0 = wave - sub;
-      if (n > 0) {
-        l = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        for (int q = 0; q < share; ++q) {
-          float x[8];
-          load8_f32(&sums[w0 + q][8 * lane], x);
-          l += sums_l[w0 + q];
+      for (int e = 0; e < 8; ++e) v[0][e] = 0.f;
+      for (int q = 0; q < share; ++q) {
+        float x[8];
+        load8_f32(&sums[wave - sub + q][8 * lane], x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += x[e];
-        }
+        for (int e = 0; e < 8; ++e) v[0][e] += x[e];
       }
     }
-    if (n > 0) {
-      const float f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= f;
-    }
-    if (in && p.lse && lane == 0 && sub == 0)
-      p.lse[grow] = n == 0 ? p.lse_full[grow] : (l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2));
+  for (int i = 0; i < TPW; ++i) {
+    const int r = wave / share + 4 * i;
+    const float f = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+    if (p.lse && held[i] && lane == 0 && sub == 0)
+      p.lse[grow[i]] = l[i] == 0.f ? -INFINITY : fmaf(m[i], p.scale, log2_hw(l[i]) * kLn2);
     typedef float f32x8_t __attribute__((ext_vector_type(8)));
-    const f32x8_t x = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+    const f32x8_t x = f32x8_t{v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5], v[i][6], v[i][7]} * f;
     const bf16x8_t a = __builtin_convertvector(x, bf16x8_t);
     const bf16x8_t b = __builtin_convertvector(x - __builtin_convertvector(a, f32x8_t), bf16x8_t);
     const uint32_t o = r * 1024 + ((lane ^ tile_key<1024>(r)) << 4);
-    if (sub == 0) {
+    if (sub == 0 && r < kTokMax) {
       *reinterpret_cast<bf16x8_t*>(smem + o) = a;
-      *reinterpret_cast<bf16x8_t*>(smem + kJoinTok * 1024 + o) = b;
+      *reinterpret_cast<bf16x8_t*>(smem + kTokMax * 1024 + o) = b;
     }
   }
   __syncthreads();
-  // columns at or past `toks` hold whatever LDS held and are not stored
+  // token columns past the workgroup's repeat others and are not stored
+  const int col = lane & 31, src = col & (kTokMax - 1);
   f32x16_t acc = f32x16_t{};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const uint32_t o = row_operand_offset<1024>(lane, s) + q * 256;
-      acc = mfma(wf[s], row_operand(smem, o), acc);
-      acc = mfma(wf[s], row_operand(smem + kJoinTok * 1024, o), acc);
-    }
-    if (q < 3)
-#pragma unroll
-      for (int s = 0; s < 8; ++s) wf[s] = *reinterpret_cast<const bf16x8_t*>(w + 128 * (q + 1) + 16 * s);
-  }
-  const int t = t0 + (lane & 31);
-  if ((lane & 31) >= toks || t < lo || t >= hi) return;
+  static_for<32>([&](auto k_c) {
+    constexpr int k = decltype(k_c)::value;
+    const uint32_t o = src * 1024 + (((2 * (k & 7) + g) ^ tile_key<1024>(src)) << 4) + (k >> 3) * 256;
+    acc = mfma(wf[k % kW], row_operand(smem, o), acc);
+    acc = mfma(wf[k % kW], row_operand(smem + kTokMax * 1024, o), acc);
+    if constexpr (k + kW < 32) wf[k % kW] = *reinterpret_cast<const bf16x8_t*>(w + 512 * (k + kW));
+  });
+  const int t = t0 + col;
+  if (col >= toks || t >= p.T || p.info[static_cast<int64_t>(t) * p.nh + h].y < 0) return;
   uint16_t* o = p.out + static_cast<int64_t>(t) * p.out_ld + h * kDv + wave * 32 + 4 * g;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     *reinterpret_cast<uint2*>(o + 8 * i) = pack4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
 }
 
+constexpr int kJoinTok = 32;
 // tokens of a joining workgroup: as many as leave two workgroups a compute unit
 int join_tokens(int T, int nh) {
   int n = kJoinTok;
@@ -625,7 +693,7 @@ int tile_rows(int64_t T, int B, int nh) {
 }
 
 struct Layout {
-  size_t q_lat, o_full, part, part_ml, info, lse_full, total;
+  size_t q_lat, o_full, part, part_ml, info, full_ml, total;
 };
 Layout layout(int64_t T, int nh) {
   auto up = [](size_t v) { return (v + 255) & ~size_t{255}; };
@@ -637,8 +705,8 @@ Layout layout(int64_t T, int nh) {
   l.part = l.o_full + up(n * kR * 4);
   l.part_ml = l.part + 2 * kGroups * rows * kR * 4;
   l.info = l.part_ml + 2 * kGroups * rows * 8;
-  l.lse_full = l.info + up(n * 8);
-  l.total = l.lse_full + up(n * 4);
+  l.full_ml = l.info + up(n * 8);
+  l.total = l.full_ml + up(n * 8);
   return l;
 }
 
@@ -707,14 +775,19 @@ extern "C" int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, con
   a.part = reinterpret_cast<float*>(w + l.part);
   a.part_ml = reinterpret_cast<float2*>(w + l.part_ml);
   a.info = reinterpret_cast<int2*>(w + l.info);
-  a.lse_full = reinterpret_cast<float*>(w + l.lse_full);
+  a.full_ml = reinterpret_cast<float2*>(w + l.full_ml);
   a.team = team_size(T, B, n_heads, rows);
   const int toks = join_tokens(T, n_heads);
   hipLaunchKernelGGL(absorb_kernel, dim3(kR / 128, n_heads, (T + kAbsorbTok - 1) / kAbsorbTok), dim3(256), 0, stream,
                      a);
   if (rows == 32) hipLaunchKernelGGL(decode_attn_kernel<1>, dim3(kGroups), dim3(128), 0, stream, a);
   else hipLaunchKernelGGL(decode_attn_kernel<2>, dim3(kGroups), dim3(256), 0, stream, a);
-  hipLaunchKernelGGL(decode_join_kernel, dim3(n_heads, (T + toks - 1) / toks), dim3(256), 0, stream, a, rows,
-                     toks);
+  auto join = [&](auto kern) {
+    hipLaunchKernelGGL(kern, dim3(n_heads, (T + toks - 1) / toks), dim3(256), 0, stream, a, rows, toks);
+  };
+  if (toks <= 4) join(decode_join_kernel<1>);
+  else if (toks == 8) join(decode_join_kernel<2>);
+  else if (toks == 16) join(decode_join_kernel<4>);
+  else join(decode_join_kernel<8>);
   return check_launch("moe_mla_decode");
 }

@@ -18,30 +18,30 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from .layer import pack_weights
 
 LATENT, ROPE, NOPE, VALUE = 512, 64, 128, 128
 QK, CACHE_ROW = NOPE + ROPE, LATENT + ROPE
 SCALE = QK ** -0.5
 
 
-def _rows(t: torch.Tensor, name: str, *inner: int) -> int:
+def _rows(t: torch.Tensor, name: str, inner: tuple) -> int:
     """Row stride of a bf16 tensor [tokens, *inner] whose tokens are dense
     inside (the tensor may be a slice of wider rows)."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise ValueError(f"{name} must be a bfloat16 tensor on the GPU")
-    if tuple(t.shape[1:]) != inner:
-        raise ValueError(f"{name} must have shape [tokens, {', '.join(map(str, inner))}], got {tuple(t.shape)}")
-    want, size = 1, 1
-    for n, s in zip(reversed(inner), reversed(t.stride()[1:])):
-        if n > 1 and s != want:
-            raise ValueError(f"{name}: a token's values must be consecutive")
-        want *= n
-        size *= n
-    return t.stride(0) if t.shape[0] > 1 else size
+    if shape[1:] != inner:
+        raise ValueError(f"{name} must have shape [tokens, {', '.join(map(str, inner))}], got {tuple(shape)}")
+    last = inner[-1]
+    if stride[-1] != 1 or (len(inner) == 2 and stride[1] != last and inner[0] > 1):
+        raise ValueError(f"{name}: a token's values must be consecutive")
+    # a lone token's stride is never used, and may be anything
+    return stride[0] if shape[0] > 1 else last * (inner[0] if len(inner) == 2 else 1)
 
 
-def _vec(t: torch.Tensor, name: str, dtype, *shape: int) -> torch.Tensor:
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+def _vec(t: torch.Tensor, name: str, dtype, shape: tuple) -> torch.Tensor:
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on the GPU, got "
                          f"{t.dtype} {tuple(t.shape)}")
     return t
@@ -75,10 +75,10 @@ class LatentAttention:
             raise ValueError(f"expected {self.Tq} queries and {self.Tk} keys")
         if not 0 <= B <= self.n_seqs:
             raise ValueError(f"cu_q must describe at most {self.n_seqs} sequences")
-        _vec(cu_q, "cu_q", torch.int32, B + 1)
-        _vec(cu_k, "cu_k", torch.int32, B + 1)
-        return (q, _rows(q, "q", h, QK), kv, _rows(kv, "kv", h, NOPE + VALUE), k_rope,
-                _rows(k_rope, "k_rope", ROPE)), B
+        _vec(cu_q, "cu_q", torch.int32, (B + 1,))
+        _vec(cu_k, "cu_k", torch.int32, (B + 1,))
+        return (q, _rows(q, "q", (h, QK)), kv, _rows(kv, "kv", (h, NOPE + VALUE)), k_rope,
+                _rows(k_rope, "k_rope", (ROPE,))), B
 
     def forward(self, q, kv, k_rope, cu_q, cu_k, stream=None):
         """out [Tq, n_heads, 128] bf16 and lse [Tq, n_heads] fp32."""
@@ -97,7 +97,7 @@ class LatentAttention:
         ins, B = self._inputs(q, kv, k_rope, cu_q, cu_k)
         if dout.shape[0] != self.Tq:
             raise ValueError(f"expected {self.Tq} rows of dout")
-        L.moe_mla_attn_bwd(dout, _rows(dout, "dout", h, VALUE), *ins, L.MOE_BF16, self.out, h * VALUE, self.lse,
+        L.moe_mla_attn_bwd(dout, _rows(dout, "dout", (h, VALUE)), *ins, L.MOE_BF16, self.out, h * VALUE, self.lse,
                            cu_q, cu_k, B, self.Tq, self.Tk, h, self.causal, self.scale, self.dq, h * QK, self.dkv,
                            h * (NOPE + VALUE), self.dk_rope, ROPE, self.ws, stream)
         return self.dq, self.dkv, self.dk_rope
@@ -106,15 +106,15 @@ class LatentAttention:
 class LatentDecode:
     """Attention over a paged latent cache for up to max_tokens new tokens of
     up to max_seqs requests a call. w_kvb [n_heads, 128 + 128, 512]: each
-    head's W_UK rows, then its W_UV rows (bf16); laid out once here."""
+    head's W_UK rows, then its W_UV rows (bf16); packed once here."""
 
     def __init__(self, w_kvb, *, max_tokens, max_seqs, scale=SCALE):
         h = w_kvb.shape[0]
         if w_kvb.dtype != torch.bfloat16 or tuple(w_kvb.shape[1:]) != (NOPE + VALUE, LATENT):
             raise ValueError("w_kvb must be a bfloat16 tensor [n_heads, 256, 512]")
         self.n_heads, self.max_tokens, self.max_seqs, self.scale = h, max_tokens, max_seqs, scale
-        self.w_uk = w_kvb[:, :NOPE].transpose(1, 2).contiguous()
-        self.w_uv = w_kvb[:, NOPE:].contiguous()
+        self.w_uk, _ = pack_weights(w_kvb[:, :NOPE].transpose(1, 2).contiguous(), None, "bf16")
+        self.w_uv, _ = pack_weights(w_kvb[:, NOPE:].contiguous(), None, "bf16")
         dev = w_kvb.device
         self.out = torch.empty((max_tokens, h, VALUE), dtype=torch.bfloat16, device=dev)
         nws = L.moe_mla_decode_workspace(max_tokens, h)
@@ -134,14 +134,14 @@ class LatentDecode:
         if cache.dtype != torch.bfloat16 or cache.dim() != 3 or cache.shape[2] != CACHE_ROW or \
                 not cache.is_contiguous():
             raise ValueError("cache must be a contiguous bfloat16 tensor [n_pages, page_size, 576]")
-        _vec(page_table, "page_table", torch.int32, B, page_table.shape[-1])
-        _vec(lens, "lens", torch.int32, B)
-        _vec(cu_q, "cu_q", torch.int32, B + 1)
+        _vec(page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
+        _vec(lens, "lens", torch.int32, (B,))
+        _vec(cu_q, "cu_q", torch.int32, (B + 1,))
         if tree_mask is not None:
-            _vec(tree_mask, "tree_mask", torch.int64, T)
+            _vec(tree_mask, "tree_mask", torch.int64, (T,))
         if lse is not None:
-            _vec(lse, "lse", torch.float32, T, h)
-        L.moe_mla_decode(q, _rows(q, "q", h, QK), self.w_uk, self.w_uv, L.MOE_BF16, cache, cache.shape[1],
+            _vec(lse, "lse", torch.float32, (T, h))
+        L.moe_mla_decode(q, _rows(q, "q", (h, QK)), self.w_uk, self.w_uv, L.MOE_BF16, cache, cache.shape[1],
                          cache.shape[0], page_table, page_table.shape[1], lens, cu_q, tree_mask, B, T, h, self.scale,
                          self.out, h * VALUE, lse, self.ws, stream)
         return self.out[:T]
@@ -157,27 +157,27 @@ def latent_cache_append(kv_a, cache, slots, *, norm_weight=None, eps=1e-6, cos=N
     T = kv_a.shape[0]
     if cache.dtype != torch.bfloat16 or cache.shape[-1] != CACHE_ROW or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous bfloat16 tensor [..., 576]")
-    kv_ld = _rows(kv_a, "kv_a", CACHE_ROW)
-    _vec(slots, "slots", torch.int64, T)
+    kv_ld = _rows(kv_a, "kv_a", (CACHE_ROW,))
+    _vec(slots, "slots", torch.int64, (T,))
     if norm_weight is not None:
-        _vec(norm_weight, "norm_weight", torch.bfloat16, LATENT)
+        _vec(norm_weight, "norm_weight", torch.bfloat16, (LATENT,))
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     max_pos = 1
     if cos is not None:
         max_pos = cos.shape[0]
-        _vec(cos, "cos", torch.float32, max_pos, ROPE // 2)
-        _vec(sin, "sin", torch.float32, max_pos, ROPE // 2)
+        _vec(cos, "cos", torch.float32, (max_pos, ROPE // 2))
+        _vec(sin, "sin", torch.float32, (max_pos, ROPE // 2))
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _vec(positions, "positions", torch.int32, T)
+        _vec(positions, "positions", torch.int32, (T,))
     h = q_ld = qo_ld = 0
     if q is not None:
         q_out = q if q_out is None else q_out
         if q.shape[0] != T or q_out.shape != q.shape:
             raise ValueError("q and q_out must hold one row per token")
         h = q.shape[1]
-        q_ld, qo_ld = _rows(q, "q", h, QK), _rows(q_out, "q_out", h, QK)
+        q_ld, qo_ld = _rows(q, "q", (h, QK)), _rows(q_out, "q_out", (h, QK))
     L.moe_mla_append(kv_a, kv_ld, L.MOE_BF16, norm_weight, eps, cos, sin, max_pos, positions, int(interleaved),
                      slots, cache, cache.numel() // CACHE_ROW, q, q_ld, q_out, qo_ld, T, h, stream)
     return q_out
