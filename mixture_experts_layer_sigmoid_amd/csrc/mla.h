@@ -111,9 +111,41 @@ __device__ __forceinline__ void static_for_impl(Fn&& f) {
 template <int N, typename Fn>
 __device__ __forceinline__ void static_for(Fn&& f) { static_for_impl<0, N>(f); }
 
+// The chunk's place enters an operand's offset only by exclusive or, on bits
+// that the tile's (256-byte aligned) address leaves clear: row operand s of
+// rows of 256 bytes lies at row operand 0's address ^ 32 s (s < 8; for rows of
+// 128 bytes s < 4), column block cb at block 0's ^ 64 cb (cb < 4; cb < 2). An
+// address is made where it is used, in the shadow of a product; kept ones
+// would not fit beside the sums (volatile: or the compiler would keep them).
+template <int X>
+__device__ __forceinline__ uint32_t xor_address(uint32_t base) {
+  if constexpr (X == 0) return base;
+  uint32_t r;
+  asm volatile("v_xor_b32 %0, %1, %2" : "=v"(r) : "n"(X), "v"(base));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
+}
+
 __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
+
+// Sums that stay in the accumulation registers from the first product to the
+// last. Ordinary code that reads one (a rescaling, the final store) would make
+// the compiler keep them in vector registers between the products and copy
+// them all back and forth in every tile, so each tile's products end in
+// keep_acc and such code reads through read_acc. The compiler does not know
+// what read_acc's instruction reads, so the products that wrote the sums have
+// to be over: acc_settled waits longer than the slowest product takes.
+__device__ __forceinline__ void keep_acc(f32x16_t& v) { asm volatile("" : "+a"(v)); }
+__device__ __forceinline__ float read_acc(float v) {
+  float r;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(r) : "a"(v));
+  return r;
+}
+__device__ __forceinline__ void acc_settled() { asm volatile("s_nop 15\n\ts_nop 15"); }
 
 // accumulator rows of k-step s (values 8 s .. 8 s + 7) as a bf16 operand
 __device__ __forceinline__ bf16x8_t pack_operand(const f32x16_t& v, int s) {

@@ -73,11 +73,13 @@ __global__ __launch_bounds__(256) void bwd_stats_kernel(BwdArgs p) {
 
 // ---- dk, dv: a wave keeps 32 keys (the lanes' columns), queries pass by ------
 constexpr int kQTile = 64;
+constexpr int kAhead = 5;                               // matrix operands read ahead
 constexpr int kKvWaves = 4;
 constexpr int kKvKeys = 32 * kKvWaves;
 constexpr int kLdsQn = kQTile * kDn * 2, kLdsQr = kQTile * kDr * 2, kLdsDo = kQTile * kDv * 2;
 constexpr int kLdsStat = kQTile * 8;
 constexpr int kLdsKvStage = kLdsQn + kLdsQr + kLdsDo + kLdsStat;
+static_assert(kLdsKvStage % 256 == 0, "operand addresses are made by exclusive or");
 
 __global__ __launch_bounds__(64 * kKvWaves) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void bwd_kv_kernel(BwdArgs p) {
@@ -94,7 +96,6 @@ void bwd_kv_kernel(BwdArgs p) {
   const int k0 = st.tile * kKvKeys;
   const int key = k0 + wave * 32 + (lane & 31);
   const int keyc = key < n_k ? key : n_k - 1;
-  const int wave_last = min(k0 + wave * 32 + 31, n_k - 1);     // its last key
   const int shift = p.causal ? n_k - n_q : n_k;                // query i sees keys <= i + shift
   const int q_first = p.causal ? max(0, k0 - shift) : 0;       // first query that sees a key of the tile
   const int t_first = q_first / kQTile;
@@ -137,26 +138,25 @@ void bwd_kv_kernel(BwdArgs p) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) vf[s] = *reinterpret_cast<const bf16x8_t*>(k + kDn + 16 * s);
   }
-  uint32_t ro256[8], ro128[4], co256[4][2], co128[2][2];
-#pragma unroll
-  for (int s = 0; s < 8; ++s) ro256[s] = row_operand_offset<256>(lane, s);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) ro128[s] = kLdsQn + row_operand_offset<128>(lane, s);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) co256[c][h] = col_operand_offset<256>(lane, c, h);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) co128[c][h] = kLdsQn + col_operand_offset<128>(lane, c, h);
-  }
+  const uint32_t ro256 = row_operand_offset<256>(lane, 0), ro128 = kLdsQn + row_operand_offset<128>(lane, 0);
+  const uint32_t co256_0 = col_operand_offset<256>(lane, 0, 0), co256_1 = col_operand_offset<256>(lane, 0, 1);
+  const uint32_t co128_0 = kLdsQn + col_operand_offset<128>(lane, 0, 0);
+  const uint32_t co128_1 = kLdsQn + col_operand_offset<128>(lane, 0, 1);
   f32x16_t dk[6], dv[4];
 #pragma unroll
-  for (int c = 0; c < 6; ++c) dk[c] = f32x16_t{};
+  for (int c = 0; c < 6; ++c) {
+    dk[c] = f32x16_t{};
+    keep_acc(dk[c]);
+  }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) dv[c] = f32x16_t{};
+  for (int c = 0; c < 4; ++c) {
+    dv[c] = f32x16_t{};
+    keep_acc(dv[c]);
+  }
   const float c2 = p.scale * kLog2e;
 
-  for (int t = t_first; t < t_end; ++t) {
+  auto tile = [&](int t, auto cut_c) {
+    constexpr bool kCut = decltype(cut_c)::value;
     uint8_t* buf = smem + ((t - t_first) & 1) * kLdsKvStage;
     put_stats(buf);                   // the other buffer's readers are a barrier behind
     wait_vmcnt<0>();
@@ -164,100 +164,143 @@ void bwd_kv_kernel(BwdArgs p) {
     if (t + 1 < t_end) load(t + 1, smem + ((t + 1 - t_first) & 1) * kLdsKvStage);
     const uint8_t* dob = buf + kLdsQn + kLdsQr;
     const float* stat = reinterpret_cast<const float*>(dob + kLdsDo);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s = mfma(row_operand(buf, ro256[k] + b * 32 * 256), kf[k], s);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s = mfma(row_operand(buf, ro128[k] + b * 32 * 128), kf[8 + k], s);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dp = mfma(row_operand(dob, ro256[k] + b * 32 * 256), vf[k], dp);
-      const int q0 = t * kQTile + 32 * b;
-      const bool cut = p.causal && q0 + shift < wave_last;
-#pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const f32x4_t l2 = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * i4 + 4 * g);
-        const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(stat + 64 + 32 * b + 8 * i4 + 4 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * i4 + e;
-          s[i] = exp2_hw(fmaf(s[i], c2, -l2[e]));
-          dp[i] = s[i] * (dp[i] - dl[e]);
+    // 80 products of two blocks of 32 queries: the scores and dp of block 0,
+    // of block 1, then dv and dk from block 0 and from block 1. Their LDS
+    // operands are read kAhead products ahead, and the element-wise work of
+    // block 0 runs between the products of block 1's scores, that of block 1
+    // between the products of block 0's gradients.
+    const uint32_t bo = static_cast<uint32_t>(buf - smem);
+    const uint32_t r256 = bo + ro256, r128 = bo + ro128, c256_0 = bo + co256_0, c256_1 = bo + co256_1;
+    const uint32_t c128_0 = bo + co128_0, c128_1 = bo + co128_1;
+    constexpr int kDo = kLdsQn + kLdsQr;                // dO's place behind Q's
+    {
+      bf16x8_t a[kAhead], pf[2][2], sf[2][2];
+      f32x16_t s[2], dp[2];
+      f32x4_t l2[2], dl[2];
+      typedef float f32x8_t __attribute__((ext_vector_type(8)));
+      f32x8_t we, de;                 // elements of the current operand
+      auto fetch = [&](auto n_c) {
+        constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+        if constexpr (n < 40) {
+          constexpr int b = n / 20, k = n % 20;
+          if constexpr (k >= 16) a[slot] = row_operand(smem, xor_address<32 * (k - 16)>(r128) + b * 32 * 128);
+          else a[slot] = row_operand(smem, xor_address<32 * (k / 2)>(r256) + (k % 2 ? kDo : 0) + b * 32 * 256);
+        } else {
+          constexpr int b = (n - 40) / 20, k = (n - 40) % 20 / 10, c = (n - 40) % 10;
+          constexpr int o256 = (2 * b + k) * 16 * 256 + (c < 4 ? kDo : 0), o128 = (2 * b + k) * 16 * 128;
+          if constexpr (c >= 8)
+            a[slot] = col_operand(smem, xor_address<64 * (c - 8)>(c128_0) + o128, xor_address<64 * (c - 8)>(c128_1) + o128);
+          else
+            a[slot] = col_operand(smem, xor_address<64 * (c % 4)>(c256_0) + o256, xor_address<64 * (c % 4)>(c256_1) + o256);
         }
-      }
-      if (cut) {
+      };
+      // statistics of 4 queries: elements 4 j .. 4 j + 3 of block b
+      auto stats_of = [&](auto b_c, auto j_c) {
+        constexpr int b = decltype(b_c)::value, j = decltype(j_c)::value;
+        l2[j & 1] = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j + 4 * g);
+        dl[j & 1] = *reinterpret_cast<const f32x4_t*>(stat + 64 + 32 * b + 8 * j + 4 * g);
+      };
+      auto element = [&](auto b_c, auto i_c) {
+        constexpr int b = decltype(b_c)::value, i = decltype(i_c)::value;
+        if constexpr (i % 4 == 0 && i < 12) stats_of(b_c, std::integral_constant<int, i / 4 + 1>{});
+        float w = exp2_hw(fmaf(s[b][i], c2, -l2[(i >> 2) & 1][i & 3]));
+        float d = w * (dp[b][i] - dl[(i >> 2) & 1][i & 3]);
+        if constexpr (kCut) {
+          const bool hidden = key > t * kQTile + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) + shift;
+          w = hidden ? 0.f : w;
+          d = hidden ? 0.f : d;
+        }
+        we[i % 8] = w;
+        de[i % 8] = d;
+        if constexpr (i % 8 == 7) {
+          pf[b][i / 8] = __builtin_convertvector(we, bf16x8_t);
+          sf[b][i / 8] = __builtin_convertvector(de, bf16x8_t);
+        }
+      };
+      static_for<kAhead>([&](auto n_c) { fetch(n_c); });
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<80>([&](auto n_c) {
+        constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+        if constexpr (n < 40) {
+          constexpr int b = n / 20, k = n % 20;
+          if constexpr (k >= 16) s[b] = mfma(a[slot], kf[8 + k - 16], s[b]);
+          else if constexpr (k % 2 == 0) s[b] = mfma(a[slot], kf[k / 2], k == 0 ? f32x16_t{} : s[b]);
+          else dp[b] = mfma(a[slot], vf[k / 2], k == 1 ? f32x16_t{} : dp[b]);
+        } else {
+          constexpr int b = (n - 40) / 20, k = (n - 40) % 20 / 10, c = (n - 40) % 10;
+          if constexpr (c < 4) dv[c] = mfma(a[slot], pf[b][k], dv[c]);
+          else dk[c - 4] = mfma(a[slot], sf[b][k], dk[c - 4]);
+        }
+        if constexpr (n + kAhead < 80) fetch(std::integral_constant<int, n + kAhead>{});
+        // element i of block b behind product 20 b + 22 + i
+        if constexpr (n >= 22 && n < 38) element(std::integral_constant<int, 0>{}, std::integral_constant<int, n - 22>{});
+        if constexpr (n == 18 || n == 38)
+          stats_of(std::integral_constant<int, n / 20>{}, std::integral_constant<int, 0>{});
+        if constexpr (n >= 42 && n < 58) element(std::integral_constant<int, 1>{}, std::integral_constant<int, n - 42>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (key > q0 + 8 * (i >> 2) + 4 * g + (i & 3) + shift) {
-            s[i] = 0.f;
-            dp[i] = 0.f;
-          }
-      }
+      for (int c = 0; c < 6; ++c) keep_acc(dk[c]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const bf16x8_t pf = pack_operand(s, k), sf = pack_operand(dp, k);
-        const int o256 = (2 * b + k) * 16 * 256, o128 = (2 * b + k) * 16 * 128;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) dv[c] = mfma(col_operand(dob, co256[c][0] + o256, co256[c][1] + o256), pf, dv[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) dk[c] = mfma(col_operand(buf, co256[c][0] + o256, co256[c][1] + o256), sf, dk[c]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          dk[4 + c] = mfma(col_operand(buf, co128[c][0] + o128, co128[c][1] + o128), sf, dk[4 + c]);
-      }
+      for (int c = 0; c < 4; ++c) keep_acc(dv[c]);
     }
-  }
+  };
+  // the tiles that the causal mask cuts come first; each loop has one body
+  // (a choice inside it would cost copies of the sums where its sides meet)
+  const int cut_end = p.causal ? min(t_end, max(t_first, (k0 + kKvKeys - shift + kQTile - 1) / kQTile)) : t_first;
+  int t = t_first;
+  for (; t < cut_end; ++t) tile(t, std::true_type{});
+  for (; t < t_end; ++t) tile(t, std::false_type{});
+  acc_settled();
   if (key >= n_k) return;
   const int64_t tok = static_cast<int64_t>(st.start) + key;
   uint16_t* o = p.dkv + tok * p.dkv_ld + head * (kDn + kDv) + 4 * g;
+  auto value = [&](const f32x16_t& v, int i) {
+    return f32x4_t{read_acc(v[4 * i]), read_acc(v[4 * i + 1]), read_acc(v[4 * i + 2]), read_acc(v[4 * i + 3])};
+  };
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float sc = p.scale;
-      *reinterpret_cast<uint2*>(o + 32 * c + 8 * i) =
-          pack4(dk[c][4 * i] * sc, dk[c][4 * i + 1] * sc, dk[c][4 * i + 2] * sc, dk[c][4 * i + 3] * sc);
-      *reinterpret_cast<uint2*>(o + kDn + 32 * c + 8 * i) =
-          pack4(dv[c][4 * i], dv[c][4 * i + 1], dv[c][4 * i + 2], dv[c][4 * i + 3]);
+      const f32x4_t x = value(dk[c], i) * p.scale, y = value(dv[c], i);
+      *reinterpret_cast<uint2*>(o + 32 * c + 8 * i) = pack4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint2*>(o + kDn + 32 * c + 8 * i) = pack4(y[0], y[1], y[2], y[3]);
     }
   float* r = p.dkr_part + (static_cast<int64_t>(head) * p.Tk + tok) * kDr + 4 * g;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<f32x4_t*>(r + 32 * c + 8 * i) =
-          f32x4_t{dk[4 + c][4 * i], dk[4 + c][4 * i + 1], dk[4 + c][4 * i + 2], dk[4 + c][4 * i + 3]};
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4_t*>(r + 32 * c + 8 * i) = value(dk[4 + c], i);
 }
 
 // ---- dq: a wave keeps 32 queries (the lanes' columns), keys pass by ----------
 constexpr int kKt = 64;
+constexpr int kQWaves = 4;
+constexpr int kQRows = 32 * kQWaves;
 constexpr int kLdsKn = kKt * kDn * 2, kLdsKr = kKt * kDr * 2, kLdsV = kKt * kDv * 2;
 constexpr int kLdsQStage = kLdsKn + kLdsKr + kLdsV;
 
-template <int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(64 * kQWaves) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void bwd_q_kernel(BwdArgs p) {
-  constexpr int kQt = 32 * NW;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kLdsQStage];
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int idx = xcd_contiguous(blockIdx.x, gridDim.x);
   const int head = idx / p.n_tiles;
-  const SeqTile st = find_tile(p.cu_q, p.B, p.Tq, kQt, p.n_tiles - 1 - idx % p.n_tiles);
+  const SeqTile st = find_tile(p.cu_q, p.B, p.Tq, kQRows, p.n_tiles - 1 - idx % p.n_tiles);
   if (st.b < 0) return;
   const int k_start = clamp_int(p.cu_k[st.b], 0, p.Tk);
   const int n_k = clamp_int(p.cu_k[st.b + 1], k_start, p.Tk) - k_start;
   const int n_q = st.n;
-  const int w0 = st.tile * kQt + wave * 32;
-  const int row = w0 + (lane & 31);
+  const int q0 = st.tile * kQRows;
+  const int row = q0 + wave * 32 + (lane & 31);
   const int rowc = row < n_q ? row : n_q - 1;
   const int shift = p.causal ? n_k - n_q : n_k;
   const int last = p.causal ? min(rowc + shift, n_k - 1) : n_k - 1;
-  const int wave_first = p.causal ? min(min(w0, n_q - 1) + shift, n_k - 1) : n_k - 1;
-  const int wave_last = p.causal ? min(min(w0 + 31, n_q - 1) + shift, n_k - 1) : n_k - 1;
-  const int tile_last = p.causal ? min(min(st.tile * kQt + kQt, n_q) - 1 + shift, n_k - 1) : n_k - 1;
+  const int first_last = p.causal ? min(q0 + shift, n_k - 1) : n_k - 1;     // of the tile's first query
+  const int tile_last = p.causal ? min(min(q0 + kQRows, n_q) - 1 + shift, n_k - 1) : n_k - 1;
   const int n_kt = tile_last < 0 ? 0 : tile_last / kKt + 1;
+  const int n_full = first_last < 0 ? 0 : min(n_kt, (first_last + 1) / kKt); // tiles that every query sees whole
 
   const uint16_t* kv = p.kv + static_cast<int64_t>(k_start) * p.kv_ld + head * (kDn + kDv);
   const uint16_t* kr = p.kr + static_cast<int64_t>(k_start) * p.kr_ld;
@@ -266,10 +309,10 @@ void bwd_q_kernel(BwdArgs p) {
     const int nv = n < kKt ? n : kKt;
     const uint16_t* b = kv + static_cast<int64_t>(kt) * kKt * p.kv_ld;
     const uint32_t ld = static_cast<uint32_t>(p.kv_ld * 2);
-    tile_load<256, kKt, NW>(b, ld, nv, buf, wave, lane);
-    tile_load<128, kKt, NW>(kr + static_cast<int64_t>(kt) * kKt * p.kr_ld, static_cast<uint32_t>(p.kr_ld * 2), nv,
-                            buf + kLdsKn, wave, lane);
-    tile_load<256, kKt, NW>(b + kDn, ld, nv, buf + kLdsKn + kLdsKr, wave, lane);
+    tile_load<256, kKt, kQWaves>(b, ld, nv, buf, wave, lane);
+    tile_load<128, kKt, kQWaves>(kr + static_cast<int64_t>(kt) * kKt * p.kr_ld, static_cast<uint32_t>(p.kr_ld * 2), nv,
+                                 buf + kLdsKn, wave, lane);
+    tile_load<256, kKt, kQWaves>(b + kDn, ld, nv, buf + kLdsKn + kLdsKr, wave, lane);
   };
   if (n_kt > 0) load(0, smem);
 
@@ -284,59 +327,82 @@ void bwd_q_kernel(BwdArgs p) {
     for (int s = 0; s < kDv / 16; ++s) df[s] = *reinterpret_cast<const bf16x8_t*>(d + 16 * s);
   }
   const float2 stat = p.stats[static_cast<int64_t>(head) * p.Tq + tokc];
-  uint32_t ro256[8], ro128[4], co256[4][2], co128[2][2];
-#pragma unroll
-  for (int s = 0; s < 8; ++s) ro256[s] = row_operand_offset<256>(lane, s);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) ro128[s] = kLdsKn + row_operand_offset<128>(lane, s);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) co256[c][h] = col_operand_offset<256>(lane, c, h);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) co128[c][h] = kLdsKn + col_operand_offset<128>(lane, c, h);
-  }
+  const uint32_t ro256 = row_operand_offset<256>(lane, 0), ro128 = kLdsKn + row_operand_offset<128>(lane, 0);
+  const uint32_t co256_0 = col_operand_offset<256>(lane, 0, 0), co256_1 = col_operand_offset<256>(lane, 0, 1);
+  const uint32_t co128_0 = kLdsKn + col_operand_offset<128>(lane, 0, 0);
+  const uint32_t co128_1 = kLdsKn + col_operand_offset<128>(lane, 0, 1);
   f32x16_t dq[6];
 #pragma unroll
-  for (int c = 0; c < 6; ++c) dq[c] = f32x16_t{};
+  for (int c = 0; c < 6; ++c) {
+    dq[c] = f32x16_t{};
+    keep_acc(dq[c]);
+  }
   const float c2 = p.scale * kLog2e;
 
-  for (int kt = 0; kt < n_kt; ++kt) {
+  auto tile = [&](int kt, auto cut_c) {
+    constexpr bool kCut = decltype(cut_c)::value;
     wait_vmcnt<0>();
     lds_barrier();
-    uint8_t* buf = smem + (kt & 1) * kLdsQStage;
+    const uint32_t bo = (kt & 1) * kLdsQStage;
     if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1) & 1) * kLdsQStage);
-    const int t0 = kt * kKt;
-    if (t0 > wave_last) continue;
-    const uint8_t* vb = buf + kLdsKn + kLdsKr;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s = mfma(row_operand(buf, ro256[k] + b * 32 * 256), qf[k], s);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s = mfma(row_operand(buf, ro128[k] + b * 32 * 128), qf[8 + k], s);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dp = mfma(row_operand(vb, ro256[k] + b * 32 * 256), df[k], dp);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) dp[i] = exp2_hw(fmaf(s[i], c2, -stat.x)) * (dp[i] - stat.y);
-      if (t0 + 32 * b + 31 > wave_first) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (t0 + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) > last) dp[i] = 0.f;
+    const uint32_t r256 = bo + ro256, r128 = bo + ro128, c256_0 = bo + co256_0, c256_1 = bo + co256_1;
+    const uint32_t c128_0 = bo + co128_0, c128_1 = bo + co128_1;
+    constexpr int kV = kLdsKn + kLdsKr;                 // V's place behind K's
+    // 64 products, in the order of the kernel above: scores and dp of block 0
+    // and block 1 of 32 keys, then dq from block 0 and from block 1; the
+    // element-wise work of a block runs between the products after its scores
+    bf16x8_t a[kAhead], sf[2][2];
+    f32x16_t s[2], dp[2];
+    typedef float f32x8_t __attribute__((ext_vector_type(8)));
+    f32x8_t de;
+    auto fetch = [&](auto n_c) {
+      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+      if constexpr (n < 40) {
+        constexpr int b = n / 20, k = n % 20;
+        if constexpr (k >= 16) a[slot] = row_operand(smem, xor_address<32 * (k - 16)>(r128) + b * 32 * 128);
+        else a[slot] = row_operand(smem, xor_address<32 * (k / 2)>(r256) + (k % 2 ? kV : 0) + b * 32 * 256);
+      } else {
+        constexpr int k = (n - 40) / 6, c = (n - 40) % 6;
+        constexpr int o256 = k * 16 * 256, o128 = k * 16 * 128;
+        if constexpr (c >= 4)
+          a[slot] = col_operand(smem, xor_address<64 * (c - 4)>(c128_0) + o128, xor_address<64 * (c - 4)>(c128_1) + o128);
+        else
+          a[slot] = col_operand(smem, xor_address<64 * c>(c256_0) + o256, xor_address<64 * c>(c256_1) + o256);
       }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const bf16x8_t sf = pack_operand(dp, k);
-        const int o256 = (2 * b + k) * 16 * 256, o128 = (2 * b + k) * 16 * 128;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) dq[c] = mfma(col_operand(buf, co256[c][0] + o256, co256[c][1] + o256), sf, dq[c]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          dq[4 + c] = mfma(col_operand(buf, co128[c][0] + o128, co128[c][1] + o128), sf, dq[4 + c]);
+    };
+    auto element = [&](auto b_c, auto i_c) {
+      constexpr int b = decltype(b_c)::value, i = decltype(i_c)::value;
+      float d = exp2_hw(fmaf(s[b][i], c2, -stat.x)) * (dp[b][i] - stat.y);
+      if constexpr (kCut) d = kt * kKt + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) > last ? 0.f : d;
+      de[i % 8] = d;
+      if constexpr (i % 8 == 7) sf[b][i / 8] = __builtin_convertvector(de, bf16x8_t);
+    };
+    static_for<kAhead>([&](auto n_c) { fetch(n_c); });
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<64>([&](auto n_c) {
+      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+      if constexpr (n < 40) {
+        constexpr int b = n / 20, k = n % 20;
+        if constexpr (k >= 16) s[b] = mfma(a[slot], qf[8 + k - 16], s[b]);
+        else if constexpr (k % 2 == 0) s[b] = mfma(a[slot], qf[k / 2], k == 0 ? f32x16_t{} : s[b]);
+        else dp[b] = mfma(a[slot], df[k / 2], k == 1 ? f32x16_t{} : dp[b]);
+      } else {
+        constexpr int k = (n - 40) / 6, c = (n - 40) % 6;
+        dq[c] = mfma(a[slot], sf[k / 2][k % 2], dq[c]);
       }
-    }
-  }
+      if constexpr (n + kAhead < 64) fetch(std::integral_constant<int, n + kAhead>{});
+      if constexpr (n >= 22 && n < 38) element(std::integral_constant<int, 0>{}, std::integral_constant<int, n - 22>{});
+      if constexpr (n >= 42 && n < 58) element(std::integral_constant<int, 1>{}, std::integral_constant<int, n - 42>{});
+      __builtin_amdgcn_sched_barrier(0);
+    });
+#pragma unroll
+    for (int c = 0; c < 6; ++c) keep_acc(dq[c]);
+  };
+  int kt = 0;
+  for (; kt < n_full; ++kt) tile(kt, std::false_type{});
+  for (; kt < n_kt; ++kt) tile(kt, std::true_type{});
+
+  acc_settled();
   if (row >= n_q) return;
   uint16_t* o = p.dq + tokc * p.dq_ld + head * kDq + 4 * g;
 #pragma unroll
@@ -345,7 +411,8 @@ void bwd_q_kernel(BwdArgs p) {
     for (int i = 0; i < 4; ++i) {
       const float sc = p.scale;
       *reinterpret_cast<uint2*>(o + 32 * c + 8 * i) =
-          pack4(dq[c][4 * i] * sc, dq[c][4 * i + 1] * sc, dq[c][4 * i + 2] * sc, dq[c][4 * i + 3] * sc);
+          pack4(read_acc(dq[c][4 * i]) * sc, read_acc(dq[c][4 * i + 1]) * sc, read_acc(dq[c][4 * i + 2]) * sc,
+                read_acc(dq[c][4 * i + 3]) * sc);
     }
 }
 
@@ -436,12 +503,9 @@ extern "C" int moe_mla_attn_bwd(const void* dout, int64_t dout_ld, const void* q
     hipLaunchKernelGGL(bwd_rope_kernel, dim3((Tk + 3) / 4), dim3(256), 0, stream, a);
   }
   if (Tq > 0) {
-    auto launch = [&](auto kern, int nw) {
-      a.n_tiles = seq_tiles_bound(B, Tq, 32 * nw);
-      hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(a.n_tiles) * n_heads), dim3(64 * nw), 0, stream, a);
-    };
-    if (Tq / B >= 512) launch(bwd_q_kernel<8>, 8);
-    else launch(bwd_q_kernel<4>, 4);
+    a.n_tiles = seq_tiles_bound(B, Tq, kQRows);
+    hipLaunchKernelGGL(bwd_q_kernel, dim3(static_cast<unsigned>(a.n_tiles) * n_heads), dim3(64 * kQWaves), 0, stream,
+                       a);
   }
   return check_launch(fn);
 }

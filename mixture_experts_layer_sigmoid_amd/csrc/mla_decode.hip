@@ -192,19 +192,6 @@ __device__ __forceinline__ void scale_operand(bf16x8_t& v, float f) {
   v = __builtin_convertvector(__builtin_convertvector(v, f32x8_t) * f, bf16x8_t);
 }
 
-// The sums stay in the accumulation registers from the first product to the
-// last. Ordinary code that reads one (the rescaling, the final store) would
-// make the compiler keep them in vector registers between the products and
-// copy all 128 back and forth in every tile, so it reads them through
-// read_acc. The reads come long after the products that wrote the sums: the
-// scores of the same tile, products issued later, have already been used.
-__device__ __forceinline__ void keep_acc(f32x16_t& v) { asm volatile("" : "+a"(v)); }
-__device__ __forceinline__ float read_acc(float v) {
-  float r;
-  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(r) : "a"(v));
-  return r;
-}
-
 // Workgroup: WR blocks of 32 rows x 2 waves. Wave (r, c) holds the queries of
 // row block r (144 registers) and the sums of latent columns 256 c .. (128
 // registers). Per token tile it scores the 32 tokens of half c, hands their
@@ -462,7 +449,7 @@ void decode_attn_kernel(DecodeArgs p) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) keep_acc(o[c]);
     }
-    asm volatile("s_nop 15\n\ts_nop 15");   // the last product's result is in its registers
+    acc_settled();
     wait_vmcnt<0>();                  // the zeros behind the last tile have arrived
     l += other_half(l);
     lds_barrier();                    // everyone is done with the buffers
