@@ -111,23 +111,6 @@ __device__ __forceinline__ void static_for_impl(Fn&& f) {
 template <int N, typename Fn>
 __device__ __forceinline__ void static_for(Fn&& f) { static_for_impl<0, N>(f); }
 
-// The chunk's place enters an operand's offset only by exclusive or, on bits
-// that the tile's (256-byte aligned) address leaves clear: row operand s of
-// rows of 256 bytes lies at row operand 0's address ^ 32 s (s < 8; for rows of
-// 128 bytes s < 4), column block cb at block 0's ^ 64 cb (cb < 4; cb < 2). An
-// address is made where it is used, in the shadow of a product; kept ones
-// would not fit beside the sums (volatile: or the compiler would keep them).
-template <int X>
-__device__ __forceinline__ uint32_t xor_address(uint32_t base) {
-  if constexpr (X == 0) return base;
-  uint32_t r;
-  asm volatile("v_xor_b32 %0, %1, %2" : "=v"(r) : "n"(X), "v"(base));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
-}
-
 __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }

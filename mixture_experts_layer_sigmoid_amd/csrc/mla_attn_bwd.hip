@@ -7,11 +7,12 @@
 //   rotary columns
 // p is computed again from the scores and the forward's lse.
 //
-// Four launches: the row statistics (lse in base 2, delta); one that keeps
-// 32 keys a wave and walks the queries (dk, dv); one that keeps 32 queries a
-// wave and walks the keys (dq); the sum of the heads' rotary gradients. The
-// scores are computed twice, so nothing is added up by atomics and the
-// result does not depend on the order in which workgroups run.
+// Three launches: the row statistics (lse in base 2, delta); the gradients,
+// where one kind of workgroup keeps 32 keys a wave and walks the queries (dk,
+// dv) and the other keeps 32 queries a wave and walks the keys (dq); the sum
+// of the heads' rotary gradients. The scores are computed twice, so nothing
+// is added up by atomics and the result does not depend on the order in which
+// workgroups run.
 #include "mla.h"
 
 #include <cmath>
@@ -44,7 +45,7 @@ struct BwdArgs {
   int64_t dkr_ld;
   float2* stats;    // [nh, Tq]: (lse in base 2, delta); a row without keys: (+inf, 0)
   float* dkr_part;  // [nh, Tk, 64]
-  int n_tiles;
+  int k_tiles, q_tiles;   // workgroups per head of the two parts
 };
 
 // 16 lanes per (token, head) row of 128 values
@@ -71,6 +72,41 @@ __global__ __launch_bounds__(256) void bwd_stats_kernel(BwdArgs p) {
   }
 }
 
+// LDS offsets of the operands of one stage: a tile of 256-byte rows, one of
+// 128-byte rows behind it (at N256), a second of 256-byte rows behind both,
+// read with the first's offsets. They move with the stage in use, so no
+// address is computed between the products.
+template <int N256>
+struct Operands {
+  uint32_t r256[8], r128[4], c256[4][2], c128[2][2];
+  __device__ __forceinline__ explicit Operands(int lane) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) r256[s] = row_operand_offset<256>(lane, s);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) r128[s] = N256 + row_operand_offset<128>(lane, s);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) c256[c][h] = col_operand_offset<256>(lane, c, h);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) c128[c][h] = N256 + col_operand_offset<128>(lane, c, h);
+    }
+  }
+  __device__ __forceinline__ void move(int by) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) r256[s] += by;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) r128[s] += by;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) c256[c][h] += by;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) c128[c][h] += by;
+    }
+  }
+};
+
 // ---- dk, dv: a wave keeps 32 keys (the lanes' columns), queries pass by ------
 constexpr int kQTile = 64;
 constexpr int kAhead = 5;                               // matrix operands read ahead
@@ -79,16 +115,12 @@ constexpr int kKvKeys = 32 * kKvWaves;
 constexpr int kLdsQn = kQTile * kDn * 2, kLdsQr = kQTile * kDr * 2, kLdsDo = kQTile * kDv * 2;
 constexpr int kLdsStat = kQTile * 8;
 constexpr int kLdsKvStage = kLdsQn + kLdsQr + kLdsDo + kLdsStat;
-static_assert(kLdsKvStage % 256 == 0, "operand addresses are made by exclusive or");
 
-__global__ __launch_bounds__(64 * kKvWaves) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void bwd_kv_kernel(BwdArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kLdsKvStage];
+__device__ __forceinline__ void bwd_kv(const BwdArgs& p, int idx, uint8_t* smem) {
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int idx = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int head = idx / p.n_tiles;
-  const SeqTile st = find_tile(p.cu_k, p.B, p.Tk, kKvKeys, idx % p.n_tiles);
+  const int head = idx / p.k_tiles;
+  const SeqTile st = find_tile(p.cu_k, p.B, p.Tk, kKvKeys, idx % p.k_tiles);
   if (st.b < 0) return;
   const int n_k = st.n;
   const int q_start = clamp_int(p.cu_q[st.b], 0, p.Tq);
@@ -138,10 +170,7 @@ void bwd_kv_kernel(BwdArgs p) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) vf[s] = *reinterpret_cast<const bf16x8_t*>(k + kDn + 16 * s);
   }
-  const uint32_t ro256 = row_operand_offset<256>(lane, 0), ro128 = kLdsQn + row_operand_offset<128>(lane, 0);
-  const uint32_t co256_0 = col_operand_offset<256>(lane, 0, 0), co256_1 = col_operand_offset<256>(lane, 0, 1);
-  const uint32_t co128_0 = kLdsQn + col_operand_offset<128>(lane, 0, 0);
-  const uint32_t co128_1 = kLdsQn + col_operand_offset<128>(lane, 0, 1);
+  Operands<kLdsQn> ops(lane);
   f32x16_t dk[6], dv[4];
 #pragma unroll
   for (int c = 0; c < 6; ++c) {
@@ -169,9 +198,6 @@ void bwd_kv_kernel(BwdArgs p) {
     // operands are read kAhead products ahead, and the element-wise work of
     // block 0 runs between the products of block 1's scores, that of block 1
     // between the products of block 0's gradients.
-    const uint32_t bo = static_cast<uint32_t>(buf - smem);
-    const uint32_t r256 = bo + ro256, r128 = bo + ro128, c256_0 = bo + co256_0, c256_1 = bo + co256_1;
-    const uint32_t c128_0 = bo + co128_0, c128_1 = bo + co128_1;
     constexpr int kDo = kLdsQn + kLdsQr;                // dO's place behind Q's
     {
       bf16x8_t a[kAhead], pf[2][2], sf[2][2];
@@ -183,15 +209,15 @@ void bwd_kv_kernel(BwdArgs p) {
         constexpr int n = decltype(n_c)::value, slot = n % kAhead;
         if constexpr (n < 40) {
           constexpr int b = n / 20, k = n % 20;
-          if constexpr (k >= 16) a[slot] = row_operand(smem, xor_address<32 * (k - 16)>(r128) + b * 32 * 128);
-          else a[slot] = row_operand(smem, xor_address<32 * (k / 2)>(r256) + (k % 2 ? kDo : 0) + b * 32 * 256);
+          if constexpr (k >= 16) a[slot] = row_operand(smem, ops.r128[k - 16] + b * 32 * 128);
+          else a[slot] = row_operand(smem, ops.r256[k / 2] + (k % 2 ? kDo : 0) + b * 32 * 256);
         } else {
           constexpr int b = (n - 40) / 20, k = (n - 40) % 20 / 10, c = (n - 40) % 10;
           constexpr int o256 = (2 * b + k) * 16 * 256 + (c < 4 ? kDo : 0), o128 = (2 * b + k) * 16 * 128;
           if constexpr (c >= 8)
-            a[slot] = col_operand(smem, xor_address<64 * (c - 8)>(c128_0) + o128, xor_address<64 * (c - 8)>(c128_1) + o128);
+            a[slot] = col_operand(smem, ops.c128[c - 8][0] + o128, ops.c128[c - 8][1] + o128);
           else
-            a[slot] = col_operand(smem, xor_address<64 * (c % 4)>(c256_0) + o256, xor_address<64 * (c % 4)>(c256_1) + o256);
+            a[slot] = col_operand(smem, ops.c256[c % 4][0] + o256, ops.c256[c % 4][1] + o256);
         }
       };
       // statistics of 4 queries: elements 4 j .. 4 j + 3 of block b
@@ -243,6 +269,7 @@ void bwd_kv_kernel(BwdArgs p) {
       for (int c = 0; c < 6; ++c) keep_acc(dk[c]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) keep_acc(dv[c]);
+      ops.move((t - t_first) & 1 ? -kLdsKvStage : kLdsKvStage);
     }
   };
   // the tiles that the causal mask cuts come first; each loop has one body
@@ -280,14 +307,11 @@ constexpr int kQRows = 32 * kQWaves;
 constexpr int kLdsKn = kKt * kDn * 2, kLdsKr = kKt * kDr * 2, kLdsV = kKt * kDv * 2;
 constexpr int kLdsQStage = kLdsKn + kLdsKr + kLdsV;
 
-__global__ __launch_bounds__(64 * kQWaves) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void bwd_q_kernel(BwdArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kLdsQStage];
+__device__ __forceinline__ void bwd_q(const BwdArgs& p, int idx, uint8_t* smem) {
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int idx = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int head = idx / p.n_tiles;
-  const SeqTile st = find_tile(p.cu_q, p.B, p.Tq, kQRows, p.n_tiles - 1 - idx % p.n_tiles);
+  const int head = idx / p.q_tiles;
+  const SeqTile st = find_tile(p.cu_q, p.B, p.Tq, kQRows, p.q_tiles - 1 - idx % p.q_tiles);
   if (st.b < 0) return;
   const int k_start = clamp_int(p.cu_k[st.b], 0, p.Tk);
   const int n_k = clamp_int(p.cu_k[st.b + 1], k_start, p.Tk) - k_start;
@@ -327,10 +351,7 @@ void bwd_q_kernel(BwdArgs p) {
     for (int s = 0; s < kDv / 16; ++s) df[s] = *reinterpret_cast<const bf16x8_t*>(d + 16 * s);
   }
   const float2 stat = p.stats[static_cast<int64_t>(head) * p.Tq + tokc];
-  const uint32_t ro256 = row_operand_offset<256>(lane, 0), ro128 = kLdsKn + row_operand_offset<128>(lane, 0);
-  const uint32_t co256_0 = col_operand_offset<256>(lane, 0, 0), co256_1 = col_operand_offset<256>(lane, 0, 1);
-  const uint32_t co128_0 = kLdsKn + col_operand_offset<128>(lane, 0, 0);
-  const uint32_t co128_1 = kLdsKn + col_operand_offset<128>(lane, 0, 1);
+  Operands<kLdsKn> ops(lane);
   f32x16_t dq[6];
 #pragma unroll
   for (int c = 0; c < 6; ++c) {
@@ -343,10 +364,7 @@ void bwd_q_kernel(BwdArgs p) {
     constexpr bool kCut = decltype(cut_c)::value;
     wait_vmcnt<0>();
     lds_barrier();
-    const uint32_t bo = (kt & 1) * kLdsQStage;
     if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1) & 1) * kLdsQStage);
-    const uint32_t r256 = bo + ro256, r128 = bo + ro128, c256_0 = bo + co256_0, c256_1 = bo + co256_1;
-    const uint32_t c128_0 = bo + co128_0, c128_1 = bo + co128_1;
     constexpr int kV = kLdsKn + kLdsKr;                 // V's place behind K's
     // 64 products, in the order of the kernel above: scores and dp of block 0
     // and block 1 of 32 keys, then dq from block 0 and from block 1; the
@@ -359,15 +377,15 @@ void bwd_q_kernel(BwdArgs p) {
       constexpr int n = decltype(n_c)::value, slot = n % kAhead;
       if constexpr (n < 40) {
         constexpr int b = n / 20, k = n % 20;
-        if constexpr (k >= 16) a[slot] = row_operand(smem, xor_address<32 * (k - 16)>(r128) + b * 32 * 128);
-        else a[slot] = row_operand(smem, xor_address<32 * (k / 2)>(r256) + (k % 2 ? kV : 0) + b * 32 * 256);
+        if constexpr (k >= 16) a[slot] = row_operand(smem, ops.r128[k - 16] + b * 32 * 128);
+        else a[slot] = row_operand(smem, ops.r256[k / 2] + (k % 2 ? kV : 0) + b * 32 * 256);
       } else {
         constexpr int k = (n - 40) / 6, c = (n - 40) % 6;
         constexpr int o256 = k * 16 * 256, o128 = k * 16 * 128;
         if constexpr (c >= 4)
-          a[slot] = col_operand(smem, xor_address<64 * (c - 4)>(c128_0) + o128, xor_address<64 * (c - 4)>(c128_1) + o128);
+          a[slot] = col_operand(smem, ops.c128[c - 4][0] + o128, ops.c128[c - 4][1] + o128);
         else
-          a[slot] = col_operand(smem, xor_address<64 * c>(c256_0) + o256, xor_address<64 * c>(c256_1) + o256);
+          a[slot] = col_operand(smem, ops.c256[c][0] + o256, ops.c256[c][1] + o256);
       }
     };
     auto element = [&](auto b_c, auto i_c) {
@@ -397,6 +415,7 @@ void bwd_q_kernel(BwdArgs p) {
     });
 #pragma unroll
     for (int c = 0; c < 6; ++c) keep_acc(dq[c]);
+    ops.move(kt & 1 ? -kLdsQStage : kLdsQStage);
   };
   int kt = 0;
   for (; kt < n_full; ++kt) tile(kt, std::false_type{});
@@ -414,6 +433,19 @@ void bwd_q_kernel(BwdArgs p) {
           pack4(read_acc(dq[c][4 * i]) * sc, read_acc(dq[c][4 * i + 1]) * sc, read_acc(dq[c][4 * i + 2]) * sc,
                 read_acc(dq[c][4 * i + 3]) * sc);
     }
+}
+
+// Both parts in one launch, dk / dv first: the second fills the compute units
+// that the first's last workgroups leave, and short sequences need both to
+// fill the chip.
+static_assert(kKvWaves == kQWaves, "one workgroup size");
+__global__ __launch_bounds__(64 * kQWaves) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void bwd_kernel(BwdArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (kLdsKvStage > kLdsQStage ? kLdsKvStage : kLdsQStage)];
+  const int n_kv = p.k_tiles * p.nh, n_q = p.q_tiles * p.nh;
+  const int id = blockIdx.x;
+  if (id < n_kv) bwd_kv(p, xcd_contiguous(id, n_kv), smem);
+  else bwd_q(p, xcd_contiguous(id - n_kv, n_q), smem);
 }
 
 // ---- dk_rope[t] = scale * sum over heads, in head order ----------------------
@@ -496,16 +528,10 @@ extern "C" int moe_mla_attn_bwd(const void* dout, int64_t dout_ld, const void* q
     const int64_t rows = static_cast<int64_t>(Tq) * n_heads;
     hipLaunchKernelGGL(bwd_stats_kernel, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, stream, a);
   }
-  if (Tk > 0) {
-    a.n_tiles = seq_tiles_bound(B, Tk, kKvKeys);
-    hipLaunchKernelGGL(bwd_kv_kernel, dim3(static_cast<unsigned>(a.n_tiles) * n_heads), dim3(64 * kKvWaves), 0,
-                       stream, a);
-    hipLaunchKernelGGL(bwd_rope_kernel, dim3((Tk + 3) / 4), dim3(256), 0, stream, a);
-  }
-  if (Tq > 0) {
-    a.n_tiles = seq_tiles_bound(B, Tq, kQRows);
-    hipLaunchKernelGGL(bwd_q_kernel, dim3(static_cast<unsigned>(a.n_tiles) * n_heads), dim3(64 * kQWaves), 0, stream,
-                       a);
-  }
+  a.k_tiles = Tk > 0 ? seq_tiles_bound(B, Tk, kKvKeys) : 0;
+  a.q_tiles = Tq > 0 ? seq_tiles_bound(B, Tq, kQRows) : 0;
+  hipLaunchKernelGGL(bwd_kernel, dim3(static_cast<unsigned>(a.k_tiles + a.q_tiles) * n_heads), dim3(64 * kQWaves), 0,
+                     stream, a);
+  if (Tk > 0) hipLaunchKernelGGL(bwd_rope_kernel, dim3((Tk + 3) / 4), dim3(256), 0, stream, a);
   return check_launch(fn);
 }

@@ -33,7 +33,7 @@ struct FwdArgs {
   int n_tiles;
 };
 
-template <int NW>
+constexpr int NW = 4;                                    // waves, 32 queries each
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void attn_fwd_kernel(FwdArgs p) {
   constexpr int kQt = 32 * NW;
@@ -195,11 +195,7 @@ extern "C" int moe_mla_attn_fwd(const void* q, int64_t q_ld, const void* kv, int
   FwdArgs a{static_cast<const uint16_t*>(q), q_ld, static_cast<const uint16_t*>(kv), kv_ld,
             static_cast<const uint16_t*>(k_rope), kr_ld, cu_q, cu_k, B, Tq, Tk, n_heads, causal, scale,
             static_cast<uint16_t*>(out), out_ld, lse, 0};
-  auto launch = [&](auto kern, int nw) {
-    a.n_tiles = seq_tiles_bound(B, Tq, 32 * nw);
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(a.n_tiles) * n_heads), dim3(64 * nw), 0, stream, a);
-  };
-  if (Tq / B >= 512) launch(attn_fwd_kernel<8>, 8);
-  else launch(attn_fwd_kernel<4>, 4);
+  a.n_tiles = seq_tiles_bound(B, Tq, 32 * NW);
+  hipLaunchKernelGGL(attn_fwd_kernel, dim3(static_cast<unsigned>(a.n_tiles) * n_heads), dim3(64 * NW), 0, stream, a);
   return check_launch("moe_mla_attn_fwd");
 }

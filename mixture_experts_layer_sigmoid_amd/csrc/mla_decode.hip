@@ -504,7 +504,7 @@ __device__ __forceinline__ float wave_max(float v) {
 template <int TPW>
 __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows, int toks) {
   constexpr int kTokMax = 4 * TPW;
-  constexpr int kUnroll = TPW >= 4 ? 1 : 4 / TPW;      // pieces of a token read at once
+  constexpr int kUnroll = 8 / TPW;                     // pieces of a token read at once
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kTokMax * kR * 2];
   __shared__ float sums[TPW == 1 ? 4 : 1][kR];
   const int lane = threadIdx.x & 63, g = lane >> 5;
@@ -552,17 +552,29 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows
   auto load_ml = [&](int i, int j) {
     return j < n[i] ? p.part_ml[piece(i, j)] : make_float2(-INFINITY, 0.f);
   };
+  // the first pieces' rows are asked for along with the pieces' statistics
+  float x[kUnroll][TPW][8];
+  auto load_rows = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int i = 0; i < TPW; ++i) {
+        const int k = j0 + u * share;
+        if (k < n[i]) load8_f32(p.part + piece(i, k) * kR + 8 * lane, x[u][i]);
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < TPW; ++i)
+    if (n[i] > 0) ml[i] = load_ml(i, lane);
+  load_rows(sub);
 #pragma unroll
   for (int i = 0; i < TPW; ++i) {
+    m[i] = ml[i].x;
+    l[i] = ml[i].y;
     if (n[i] > 0) {
-      ml[i] = load_ml(i, lane);
-      m[i] = ml[i].x;
       for (int j = 64 + lane; j < n[i]; j += 64) m[i] = fmaxf(m[i], load_ml(i, j).x);
       m[i] = wave_max(m[i]);
       l[i] = 0.f;
-    } else {
-      m[i] = ml[i].x;
-      l[i] = ml[i].y;
     }
     // a whole row counts once where several waves share a token
     const bool keep = n[i] == 0 && sub == 0;
@@ -580,20 +592,13 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows
     }
     const int c_end = min(64, n_max - c0);
     for (int j = sub; j < c_end; j += kUnroll * share) {
-      float x[kUnroll][TPW][8];
+      if (c0 + j != sub) load_rows(c0 + j);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (int i = 0; i < TPW; ++i) {
           const int k = j + u * share;
-          if (k < c_end && c0 + k < n[i]) load8_f32(p.part + piece(i, c0 + k) * kR + 8 * lane, x[u][i]);
-        }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int i = 0; i < TPW; ++i) {
-          const int k = j + u * share;
-          if (k >= c_end || c0 + k >= n[i]) continue;
+          if (k >= 64 || c0 + k >= n[i]) continue;
           const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(a[i]), k));
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[i][e] = fmaf(x[u][i][e], f, v[i][e]);
