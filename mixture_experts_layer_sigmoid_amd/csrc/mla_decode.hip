@@ -192,14 +192,15 @@ __device__ __forceinline__ void scale_operand(bf16x8_t& v, float f) {
   v = __builtin_convertvector(__builtin_convertvector(v, f32x8_t) * f, bf16x8_t);
 }
 
-// Workgroup: WR blocks of 32 rows x 2 waves. Wave (r, c) holds the queries of
-// row block r (144 registers) and the sums of latent columns 256 c .. (128
-// registers). Per token tile it scores the 32 tokens of half c, hands their
-// weights to its partner through LDS and multiplies all 64 tokens' weights
-// with its columns. (32 rows x all 512 columns per wave would need 400
-// registers for the kept operands alone, and spills.)
-// The two halves' weights refer to each wave's own running maximum; where
-// one grew, both are brought to the larger before the product.
+// Workgroup: WR blocks of 32 rows, 2 WR waves. Wave (r, c) holds the queries
+// of row block r (144 registers) and scores the 32 tokens of half c of a token
+// tile; the weights go through LDS, and every wave multiplies all rows'
+// weights with its share of the latent columns (512 / waves; 128 registers of
+// sums), so that a value operand read from LDS serves every row block. (32
+// rows x all 512 columns a wave would need 400 registers for the kept operands
+// alone, and spills; 32 rows x 256 columns reads the values twice.)
+// The halves' weights refer to each wave's own running reference; where one
+// moved, both are brought to the larger before the product.
 constexpr int kXchg = 64 * 32;                        // bytes of one wave's weights
 template <int WR>
 __global__ __launch_bounds__(128 * WR) __attribute__((amdgpu_waves_per_eu(1, 1)))
@@ -207,6 +208,7 @@ void decode_attn_kernel(DecodeArgs p) {
   constexpr int NW = 2 * WR;
   constexpr int kRows = 32 * WR;
   constexpr int kRpw = kTok / NW;                     // token rows a wave loads
+  constexpr int kCols = kR / NW, kCb = kCols / 32;    // latent columns of a wave, blocks of 32
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kTile + NW * kXchg + NW * 128];
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -232,7 +234,7 @@ void decode_attn_kernel(DecodeArgs p) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) v_off[c][h] = col_operand_offset<1024>(lane, c, h) + wc * 512;
+    for (int h = 0; h < 2; ++h) v_off[c][h] = col_operand_offset<1024>(lane, c, h) + wave * (kCols * 2);
   const float c2 = p.scale * kLog2e;
 
   while (u < u_end) {
@@ -316,13 +318,17 @@ void decode_attn_kernel(DecodeArgs p) {
       for (int s = 0; s < 4; ++s) qf[32 + s] = *reinterpret_cast<const bf16x8_t*>(qr + 16 * s);
     }
     const uint64_t sees = p.tree ? p.tree[sq.q0 + tok] : 0u;
-    f32x16_t o[8];
+    f32x16_t o[WR][kCb];
+    float m[WR], l = 0.f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      o[c] = f32x16_t{};
-      keep_acc(o[c]);
+    for (int r = 0; r < WR; ++r) {
+      m[r] = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kCb; ++c) {
+        o[r][c] = f32x16_t{};
+        keep_acc(o[r][c]);
+      }
     }
-    float m = -INFINITY, l = 0.f;
 
     for (int kt = kt0; any && kt < kt1; ++kt) {
       uint8_t* buf = smem + ((kt - kt0) & 1) * kTile;
@@ -336,7 +342,7 @@ void decode_attn_kernel(DecodeArgs p) {
       asm volatile("" : "+s"(next_ofs));                        // not one register per row
       const int t0 = kt * kTok;
       // scores: operands read kAhead steps ahead; the next tile's rows are
-      // issued between the products
+      // issued while the first operands arrive and between the products
       f32x16_t s = f32x16_t{};
       {
         bf16x8_t a[kAhead];
@@ -347,12 +353,14 @@ void decode_attn_kernel(DecodeArgs p) {
         };
         static_for<kAhead>([&](auto k_c) { fetch(k_c); });
         load_rope(next_addr);
+        static_for<kRpw / 2>([&](auto i_c) { load_row(next_bytes, next_addr, smem + next_ofs, decltype(i_c)::value); });
         __builtin_amdgcn_sched_barrier(0);
         static_for<36>([&](auto k_c) {
           constexpr int k = decltype(k_c)::value;
           s = mfma(a[k % kAhead], qf[k], s);
           if constexpr (k + kAhead < 36) fetch(std::integral_constant<int, k + kAhead>{});
-          if constexpr (k < kRpw) load_row(next_bytes, next_addr, smem + next_ofs, k);
+          if constexpr (k % 2 == 1 && k / 2 < kRpw / 2)
+            load_row(next_bytes, next_addr, smem + next_ofs, kRpw / 2 + k / 2);
           __builtin_amdgcn_sched_barrier(0);
         });
         find_page(kt + 2);
@@ -379,7 +387,9 @@ void decode_attn_kernel(DecodeArgs p) {
 #pragma unroll
       for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
       mx = fmaxf(mx, other_half(mx));
-      const float ref = next_ref(m, mx, c2);
+      float m_own = m[0];
+      if (WR == 2 && wr == 1) m_own = m[WR - 1];
+      const float ref = next_ref(m_own, mx, c2);
       // rows that have seen no key yet keep -inf: exponents against 0
       const float rc = ref == -INFINITY ? 0.f : ref * c2;
       float sum = 0.f;
@@ -388,11 +398,19 @@ void decode_attn_kernel(DecodeArgs p) {
         s[i] = exp2_hw(fmaf(s[i], c2, -rc));
         sum += s[i];
       }
-      bf16x8_t pf[2][2];              // [half][k-step]
+      bf16x8_t pf[WR][4];             // [row block][k-step of 16 tokens]
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         *reinterpret_cast<bf16x8_t*>(xw + wave * kXchg + k * 1024 + lane * 16) = pack_operand(s, k);
       if (g == 0) xref[wave * 32 + lane] = ref;
+      constexpr int kN = 4 * kCb;     // value operands: k-step of 16 tokens, column block
+      bf16x8_t va[kAhead];
+      auto fetch_v = [&](auto n_c) {
+        constexpr int n = decltype(n_c)::value, k = n / kCb, c = n % kCb;
+        va[n % kAhead] = col_operand(buf, v_off[c & 3][0] + (c >> 2) * 256 + k * 16 * 1024,
+                                     v_off[c & 3][1] + (c >> 2) * 256 + k * 16 * 1024);
+      };
+      static_for<kAhead>([&](auto n_c) { fetch_v(n_c); });
       lds_barrier();
       if (tail && (p.tree || sq.nq > 1)) {
         // a hidden token's row is still in the value product, with weight 0:
@@ -403,51 +421,47 @@ void decode_attn_kernel(DecodeArgs p) {
           if (drop_nonfinite(v)) *reinterpret_cast<u32x4_t*>(buf + i * 16) = v;
         }
         lds_barrier();
+        static_for<kAhead>([&](auto n_c) { fetch_v(n_c); });
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int r = 0; r < WR; ++r) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          pf[h][k] = *reinterpret_cast<const bf16x8_t*>(xw + (wave - wc + h) * kXchg + k * 1024 + lane * 16);
-      const float refp = xref[(wave ^ 1) * 32 + (lane & 31)];
-      const float mn = fmaxf(ref, refp);
-      if (__any(mn > m)) {
-        const float mc = mn == -INFINITY ? 0.f : mn * c2;
-        const float a = exp2_hw(fmaf(m, c2, -mc));
-        const float fo = exp2_hw(fmaf(ref, c2, -mc)), fp = exp2_hw(fmaf(refp, c2, -mc));
-        l *= a;
-        sum *= fo;
+        for (int k = 0; k < 4; ++k)
+          pf[r][k] = *reinterpret_cast<const bf16x8_t*>(xw + (2 * r + k / 2) * kXchg + (k % 2) * 1024 + lane * 16);
+        const float ref0 = xref[2 * r * 32 + (lane & 31)], ref1 = xref[(2 * r + 1) * 32 + (lane & 31)];
+        const float mn = fmaxf(ref0, ref1);
+        if (__any(mn > m[r])) {
+          const float mc = mn == -INFINITY ? 0.f : mn * c2;
+          const float a = exp2_hw(fmaf(m[r], c2, -mc));
+          const float f0 = exp2_hw(fmaf(ref0, c2, -mc)), f1 = exp2_hw(fmaf(ref1, c2, -mc));
+          if (r == wr) {
+            l *= a;
+            sum *= wc == 0 ? f0 : f1;
+          }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int k = 0; k < 4; ++k) scale_operand(pf[r][k], k < 2 ? f0 : f1);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) scale_operand(pf[h][k], h == wc ? fo : fp);
+          for (int c = 0; c < kCb; ++c) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[c][i] = read_acc(o[c][i]) * a;
-          keep_acc(o[c]);
+            for (int i = 0; i < 16; ++i) o[r][c][i] = read_acc(o[r][c][i]) * a;
+            keep_acc(o[r][c]);
+          }
+          m[r] = mn;
         }
-        m = mn;
       }
       l += sum;
-      {
-        bf16x8_t a[kAhead];
-        auto fetch = [&](auto n_c) {
-          constexpr int n = decltype(n_c)::value, k = n / 8, c = n % 8;
-          a[n % kAhead] = col_operand(buf, v_off[c & 3][0] + (c >> 2) * 256 + k * 16 * 1024,
-                                      v_off[c & 3][1] + (c >> 2) * 256 + k * 16 * 1024);
-        };
-        static_for<kAhead>([&](auto n_c) { fetch(n_c); });
-        __builtin_amdgcn_sched_barrier(0);
-        static_for<32>([&](auto n_c) {
-          constexpr int n = decltype(n_c)::value, k = n / 8, c = n % 8;
-          o[c] = mfma(a[n % kAhead], pf[k >> 1][k & 1], o[c]);
-          if constexpr (n + kAhead < 32) fetch(std::integral_constant<int, n + kAhead>{});
-          __builtin_amdgcn_sched_barrier(0);
-        });
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<kN>([&](auto n_c) {
+        constexpr int n = decltype(n_c)::value, k = n / kCb, c = n % kCb;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) keep_acc(o[c]);
+        for (int r = 0; r < WR; ++r) o[r][c] = mfma(va[n % kAhead], pf[r][k], o[r][c]);
+        if constexpr (n + kAhead < kN) fetch_v(std::integral_constant<int, n + kAhead>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+#pragma unroll
+      for (int r = 0; r < WR; ++r)
+#pragma unroll
+        for (int c = 0; c < kCb; ++c) keep_acc(o[r][c]);
     }
     acc_settled();
     wait_vmcnt<0>();                  // the zeros behind the last tile have arrived
@@ -455,31 +469,54 @@ void decode_attn_kernel(DecodeArgs p) {
     lds_barrier();                    // everyone is done with the buffers
     if (g == 0) xref[wave * 32 + lane] = l;
     lds_barrier();
-    // in the same order in both waves
-    l = xref[(wave & ~1) * 32 + (lane & 31)] + xref[(wave | 1) * 32 + (lane & 31)];
+    float lr[WR];                     // of every row block, added in the same order in all waves
+#pragma unroll
+    for (int r = 0; r < WR; ++r) lr[r] = xref[2 * r * 32 + (lane & 31)] + xref[(2 * r + 1) * 32 + (lane & 31)];
     lds_barrier();
-    if (row < n_rows) {
-      const bool writer = wc == 0 && g == 0;
-      const int64_t pr = static_cast<int64_t>(slot) * kRows + wr * 32 + (lane & 31);
-      float* dst = whole ? p.o_full + grow * kR : p.part + pr * kR;
-      if (writer) {
-        *(whole ? p.full_ml + grow : p.part_ml + pr) = make_float2(m, l);
+    // The sums leave through LDS (each wave its own part of the tile
+    // buffers), so that a row's columns are written as consecutive bytes: from
+    // the registers, every store would touch 32 rows, and that took longer
+    // than several token tiles.
+    constexpr int kRowB = kCols * 4 + 16;
+    static_assert(NW * kRows * kRowB <= 2 * kTile, "sums fit the tile buffers");
+    uint8_t* ob = smem + wave * kRows * kRowB;
+#pragma unroll
+    for (int r = 0; r < WR; ++r)
+#pragma unroll
+      for (int c = 0; c < kCb; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4_t*>(ob + (r * 32 + (lane & 31)) * kRowB + (32 * c + 8 * i + 4 * g) * 4) =
+              f32x4_t{read_acc(o[r][c][4 * i]), read_acc(o[r][c][4 * i + 1]), read_acc(o[r][c][4 * i + 2]),
+                      read_acc(o[r][c][4 * i + 3])};
+    const int64_t row0 = static_cast<int64_t>(sq.q0) * p.nh + rt * kRows;       // first row in o_full
+    const int64_t part0 = static_cast<int64_t>(slot) * kRows;
+    const int n_out = min(kRows, n_rows - rt * kRows);
+    float* dst = (whole ? p.o_full + row0 * kR : p.part + part0 * kR) + wave * kCols;
+    constexpr int kLpr = kCols / 4;                            // lanes a row
+#pragma unroll 8
+    for (int r0 = 0; r0 < kRows; r0 += 64 / kLpr) {
+      const int r = r0 + lane / kLpr, c = lane % kLpr;
+      if (r < n_out)
+        *reinterpret_cast<f32x4_t*>(dst + static_cast<int64_t>(r) * kR + 4 * c) =
+            *reinterpret_cast<const f32x4_t*>(ob + r * kRowB + 16 * c);
+    }
+    if (wave == 0 && g == 0) {
+#pragma unroll
+      for (int r = 0; r < WR; ++r) {
+        const int lr_ = r * 32 + lane;
+        if (lr_ >= n_out) continue;
+        *(whole ? p.full_ml + row0 + lr_ : p.part_ml + part0 + lr_) = make_float2(m[r], lr[r]);
         if (kt0 == 0) {
           // pieces of the row tile: this one and one of each following team
           // up to the one that holds the last token tile
           const int last_unit = first + (rg + 1) * sq.tok_tiles - 1;
           const int n = whole ? 0 : last_unit / per - my_team + 1;
-          p.info[grow] = make_int2(slot, n | (wr * 32 + lane) << 16);
+          p.info[row0 + lr_] = make_int2(slot, n | lr_ << 16);
         }
       }
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<f32x4_t*>(dst + 256 * wc + 32 * c + 8 * i + 4 * g) =
-              f32x4_t{read_acc(o[c][4 * i]), read_acc(o[c][4 * i + 1]), read_acc(o[c][4 * i + 2]),
-                      read_acc(o[c][4 * i + 3])};
     }
+    lds_barrier();                    // before the next piece's tiles
   }
 }
 
