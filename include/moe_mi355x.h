@@ -775,8 +775,8 @@ size_t moe_mla_decode_workspace(int T, int n_heads);
  *          fp32. A token that sees nothing gives out 0 and lse -inf.
  * ws       moe_mla_decode_workspace(T, n_heads) bytes.
  * Limits: B <= 65536, T * n_heads <= 2^24, page_size * n_pages and page_size
- * * max_pages < 2^31, (T * n_heads / 32 + B) * page_size * max_pages / 64 <
- * 2^30. B == 0 or T == 0 is a no-op.
+ * * max_pages < 2^31, (T * n_heads / 32 + B) * (page_size * max_pages / 64 +
+ * 5) < 2^30. B == 0 or T == 0 is a no-op.
  */
 int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, const void* w_uv,
                    int fmt, const void* cache, int page_size, int n_pages,

@@ -22,6 +22,7 @@ namespace {
 constexpr int kTok = 64;                               // cached tokens per tile
 constexpr int kLat = kTok * kR * 2, kRope = kTok * kDr * 2, kTile = kLat + kRope;
 constexpr int kAhead = 6;                              // matrix operands read ahead
+constexpr int kPieceCost = 4;
 constexpr int kGroups = 256;                           // workgroups of the attention
 
 struct DecodeArgs {
@@ -106,9 +107,12 @@ __global__ __launch_bounds__(256) void absorb_kernel(DecodeArgs p) {
 // Sequence b's new tokens and heads are n_q nh rows in ceil(n_q nh / rows)
 // row tiles; each row tile has to pass max(1, ceil(len / 64)) token tiles.
 // Neighbouring row tiles pass the same cached tokens, so `team` of them are
-// taken by as many workgroups of one XCD in step, and share its L2: the
-// (sequence, group of `team` row tiles, token tile) units in that order are
-// cut into equal runs, one for each team.
+// taken by as many workgroups of one XCD in step, and share its L2. In the
+// order sequence, group of `team` row tiles, token tile, every group is
+// kPieceCost + its token tiles long (a group's start and end cost about as
+// much as four tiles: queries in, sums out), and the whole is cut into equal
+// runs, one for each team. A run's piece of a group is the token tiles in it;
+// the part of a run in front of them stands for no work.
 struct Seq {
   int q0, nq, len, tok_tiles, units;
 };
@@ -120,7 +124,7 @@ __device__ __forceinline__ Seq load_seq(const DecodeArgs& p, int b, int rows) {
     s.len = clamp_int(p.lens[b], 0, p.max_pages * p.page_size);
     const int per = rows * p.team;
     s.tok_tiles = s.len > 0 ? (s.len + kTok - 1) / kTok : 1;
-    s.units = (s.nq * p.nh + per - 1) / per * s.tok_tiles;
+    s.units = (s.nq * p.nh + per - 1) / per * (s.tok_tiles + kPieceCost);
   }
   return s;
 }
@@ -202,7 +206,9 @@ __device__ __forceinline__ void scale_operand(bf16x8_t& v, float f) {
 // The halves' weights refer to each wave's own running reference; where one
 // moved, both are brought to the larger before the product.
 constexpr int kXchg = 64 * 32;                        // bytes of one wave's weights
-template <int WR>
+// kRun: every run of kRpw token rows that a wave loads lies in one page, and
+// takes one buffer resource (any other page size: one a row).
+template <int WR, bool kRun>
 __global__ __launch_bounds__(128 * WR) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void decode_attn_kernel(DecodeArgs p) {
   constexpr int NW = 2 * WR;
@@ -240,20 +246,21 @@ void decode_attn_kernel(DecodeArgs p) {
   while (u < u_end) {
     int b, first;
     const Seq sq = find_unit(p, kRows, seqs, u, b, first);
-    const int rg = (u - first) / sq.tok_tiles;
-    const int kt0 = (u - first) - rg * sq.tok_tiles;
-    const int kt1 = min(sq.tok_tiles, kt0 + (u_end - u));      // token tiles [kt0, kt1) of this row tile
+    const int len_g = sq.tok_tiles + kPieceCost;
+    const int rg = (u - first) / len_g;
+    const int x0 = (u - first) - rg * len_g, x1 = min(len_g, x0 + (u_end - u));
+    const int kt0 = max(0, x0 - kPieceCost), kt1 = max(0, x1 - kPieceCost);  // token tiles [kt0, kt1)
     const bool whole = kt0 == 0 && kt1 == sq.tok_tiles;
     const int rt = rg * p.team + member;
     const int slot = 2 * grp + (u == u_begin ? 0 : 1);
-    u += kt1 - kt0;
+    u += x1 - x0;
+    if (kt0 == kt1) continue;
 
     const int n_rows = sq.nq * p.nh;
     if (rt * kRows >= n_rows) continue;                         // the last group has fewer row tiles
     const int row = rt * kRows + wr * 32 + (lane & 31);
     const int rowc = min(row, n_rows - 1);
     const int tok = rowc / p.nh;                                // new token of the row
-    const int64_t grow = static_cast<int64_t>(sq.q0) * p.nh + rowc;
     const int prefix = sq.len - sq.nq;                          // cached tokens before the new ones
 
     // Page and place of the wave's token rows, lane i: row wave * kRpw + i
@@ -271,13 +278,25 @@ void decode_attn_kernel(DecodeArgs p) {
       const int slot = clamp_int(page, 0, p.n_pages - 1) * p.page_size + place;
       return reinterpret_cast<uint64_t>(p.cache) + static_cast<uint64_t>(slot) * (kDc * 2);
     };
-    // row i of the wave's share into lds: 64 lanes x 16 bytes (zeros if
-    // `bytes` is 0)
-    auto load_row = [&](uint32_t bytes, uint64_t addr, uint8_t* lds, int i) {
-      const uint64_t a = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr), i)) & 0xFFFFFFFFu;
-      const uint64_t h = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr >> 32), i)) << 32;
-      const __amdgpu_buffer_rsrc_t rs = buf_rsrc(reinterpret_cast<const void*>(h | a), bytes);
-      lds_load16_buf(rs, (lane ^ tile_key<1024>(i)) << 4, 0, lds + i * 1024);   // kRpw % 16 == 0: key(row) = key(i)
+    // Row i of the wave's share into lds: 64 lanes x 16 bytes. With kRun,
+    // `rs` holds the share's valid rows and the others come as zeros; else
+    // `addr` the rows' addresses and `bytes` 0 asks for zeros.
+    auto load_row = [&](__amdgpu_buffer_rsrc_t rs, uint32_t bytes, uint64_t addr, uint8_t* lds, int i) {
+      if constexpr (kRun) {
+        lds_load16_buf(rs, ((lane ^ tile_key<1024>(i)) << 4) + i * (kDc * 2), 0, lds + i * 1024);
+      } else {
+        const uint64_t a = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr), i)) & 0xFFFFFFFFu;
+        const uint64_t h = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr >> 32), i)) << 32;
+        lds_load16_buf(buf_rsrc(reinterpret_cast<const void*>(h | a), bytes), (lane ^ tile_key<1024>(i)) << 4, 0,
+                       lds + i * 1024);                          // kRpw % 16 == 0: key(row) = key(i)
+      }
+    };
+    // the resource of the share's rows in token tile kt
+    auto run_rsrc = [&](int kt, uint64_t addr) {
+      const uint64_t a = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr), 0)) & 0xFFFFFFFFu;
+      const uint64_t h = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr >> 32), 0)) << 32;
+      const int n = kt < kt1 ? clamp_int(sq.len - kt * kTok - wave * kRpw, 0, kRpw) : 0;
+      return buf_rsrc(reinterpret_cast<const void*>(h | a), n > 0 ? (n - 1) * (kDc * 2) + kR * 2 : 0);
     };
     u32x4_t rope[kRpw / 8];
     auto load_rope = [&](uint64_t addr) {
@@ -304,18 +323,42 @@ void decode_attn_kernel(DecodeArgs p) {
       find_page(kt0);
       const uint64_t a0 = row_address();
       load_rope(a0);
+      const __amdgpu_buffer_rsrc_t rs = run_rsrc(kt0, a0);
 #pragma unroll
-      for (int i = 0; i < kRpw; ++i) load_row(kR * 2, a0, smem + w_row * 1024, i);
+      for (int i = 0; i < kRpw; ++i) load_row(rs, kR * 2, a0, smem + w_row * 1024, i);
       find_page(kt0 + 1);
     }
+    // The queries come through the second tile buffer, like cached rows (64
+    // or 32 consecutive rows of q_lat, and the rows' rotary parts): read from
+    // memory as operands, each load would touch 32 rows.
     bf16x8_t qf[kDc / 16];
-    {
-      const uint16_t* ql = p.q_lat + grow * kR + 8 * g;
-      const uint16_t* qr = p.q + (static_cast<int64_t>(sq.q0) + tok) * p.q_ld + (rowc - tok * p.nh) * kDq + kDn + 8 * g;
+    if (any) {
+      uint8_t* qb = smem + kTile;
+      constexpr int kQr = kRows / NW;                            // rows a wave loads
+      const int q_row = wave * kQr;
+      const int64_t first_row = static_cast<int64_t>(sq.q0) * p.nh + rt * kRows;
+      const int n_valid = clamp_int(n_rows - rt * kRows - q_row, 0, kQr);
+      const __amdgpu_buffer_rsrc_t rs = buf_rsrc(p.q_lat + (first_row + q_row) * kR, n_valid * kR * 2);
 #pragma unroll
-      for (int s = 0; s < 32; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(ql + 16 * s);
+      for (int i = 0; i < kQr; ++i)
+        lds_load16_buf(rs, ((lane ^ tile_key<1024>(q_row + i)) << 4) + i * kR * 2, 0, qb + (q_row + i) * 1024);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) qf[32 + s] = *reinterpret_cast<const bf16x8_t*>(qr + 16 * s);
+      for (int i = 0; i < kQr / 8; ++i) {
+        const int r = q_row + i * 8 + (lane >> 3);
+        const int rr = min(rt * kRows + r, n_rows - 1), t = rr / p.nh;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(
+            p.q + (static_cast<int64_t>(sq.q0) + t) * p.q_ld + (rr - t * p.nh) * kDq + kDn + (lane & 7) * 8);
+        *reinterpret_cast<u32x4_t*>(qb + kLat + r * 128 + (((lane & 7) ^ tile_key<128>(r)) << 4)) = v;
+      }
+      wait_vmcnt<0>();
+      lds_barrier();
+      // lat_off / rope_off are those of token half wc; here the row block is wr
+      const int to_block = (wr - wc) * 32;
+#pragma unroll
+      for (int s = 0; s < 32; ++s)
+        qf[s] = row_operand(qb, lat_off[s & 7] + (s >> 3) * 256 + to_block * 1024);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) qf[32 + s] = row_operand(qb, rope_off[s] + to_block * 128);
     }
     const uint64_t sees = p.tree ? p.tree[sq.q0 + tok] : 0u;
     f32x16_t o[WR][kCb];
@@ -338,6 +381,7 @@ void decode_attn_kernel(DecodeArgs p) {
       // the next tile's rows (zeros behind the last)
       const uint32_t next_bytes = kt + 1 < kt1 ? kR * 2 : 0;
       const uint64_t next_addr = row_address();
+      const __amdgpu_buffer_rsrc_t next_rs = run_rsrc(kt + 1, next_addr);
       uint32_t next_ofs = ((kt + 1 - kt0) & 1) * kTile + w_row * 1024;
       asm volatile("" : "+s"(next_ofs));                        // not one register per row
       const int t0 = kt * kTok;
@@ -353,14 +397,14 @@ void decode_attn_kernel(DecodeArgs p) {
         };
         static_for<kAhead>([&](auto k_c) { fetch(k_c); });
         load_rope(next_addr);
-        static_for<kRpw / 2>([&](auto i_c) { load_row(next_bytes, next_addr, smem + next_ofs, decltype(i_c)::value); });
+        static_for<kRpw / 2>([&](auto i_c) { load_row(next_rs, next_bytes, next_addr, smem + next_ofs, decltype(i_c)::value); });
         __builtin_amdgcn_sched_barrier(0);
         static_for<36>([&](auto k_c) {
           constexpr int k = decltype(k_c)::value;
           s = mfma(a[k % kAhead], qf[k], s);
           if constexpr (k + kAhead < 36) fetch(std::integral_constant<int, k + kAhead>{});
           if constexpr (k % 2 == 1 && k / 2 < kRpw / 2)
-            load_row(next_bytes, next_addr, smem + next_ofs, kRpw / 2 + k / 2);
+            load_row(next_rs, next_bytes, next_addr, smem + next_ofs, kRpw / 2 + k / 2);
           __builtin_amdgcn_sched_barrier(0);
         });
         find_page(kt + 2);
@@ -510,7 +554,7 @@ void decode_attn_kernel(DecodeArgs p) {
         if (kt0 == 0) {
           // pieces of the row tile: this one and one of each following team
           // up to the one that holds the last token tile
-          const int last_unit = first + (rg + 1) * sq.tok_tiles - 1;
+          const int last_unit = first + (rg + 1) * len_g - 1;
           const int n = whole ? 0 : last_unit / per - my_team + 1;
           p.info[row0 + lr_] = make_int2(slot, n | lr_ << 16);
         }
@@ -776,7 +820,7 @@ extern "C" int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, con
   if (B == 0 || T == 0) return MOE_OK;
   const int rows = tile_rows(T, B, n_heads);
   const int64_t tiles = static_cast<int64_t>(T) * n_heads / rows + B;
-  MOE_REQUIRE(tiles * ((static_cast<int64_t>(page_size) * max_pages + kTok - 1) / kTok) < (int64_t{1} << 30),
+  MOE_REQUIRE(tiles * ((static_cast<int64_t>(page_size) * max_pages + kTok - 1) / kTok + kPieceCost) < (int64_t{1} << 30),
               MOE_ERR_INVALID_ARG, "moe_mla_decode: too much work for one call (row tiles x cached tiles >= 2^30)");
   MOE_REQUIRE(q && w_uk && w_uv && cache && page_table && lens && cu_q && out, MOE_ERR_INVALID_ARG,
               "moe_mla_decode: null pointer");
@@ -809,8 +853,16 @@ extern "C" int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, con
   const int toks = join_tokens(T, n_heads);
   hipLaunchKernelGGL(absorb_kernel, dim3(kR / 128, n_heads, (T + kAbsorbTok - 1) / kAbsorbTok), dim3(256), 0, stream,
                      a);
-  if (rows == 32) hipLaunchKernelGGL(decode_attn_kernel<1>, dim3(kGroups), dim3(128), 0, stream, a);
-  else hipLaunchKernelGGL(decode_attn_kernel<2>, dim3(kGroups), dim3(256), 0, stream, a);
+  auto attend = [&](auto kern, int waves) {
+    hipLaunchKernelGGL(kern, dim3(kGroups), dim3(64 * waves), 0, stream, a);
+  };
+  if (rows == 32) {
+    if (page_size % 32 == 0) attend(decode_attn_kernel<1, true>, 2);
+    else attend(decode_attn_kernel<1, false>, 2);
+  } else {
+    if (page_size % 16 == 0) attend(decode_attn_kernel<2, true>, 4);
+    else attend(decode_attn_kernel<2, false>, 4);
+  }
   auto join = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3(n_heads, (T + toks - 1) / toks), dim3(256), 0, stream, a, rows, toks);
   };
