@@ -296,7 +296,9 @@ void decode_attn_kernel(DecodeArgs p) {
       const uint64_t a = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr), 0)) & 0xFFFFFFFFu;
       const uint64_t h = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(addr >> 32), 0)) << 32;
       const int n = kt < kt1 ? clamp_int(sq.len - kt * kTok - wave * kRpw, 0, kRpw) : 0;
-      return buf_rsrc(reinterpret_cast<const void*>(h | a), n > 0 ? (n - 1) * (kDc * 2) + kR * 2 : 0);
+      // (the same in all lanes; said so, or each load becomes a loop over them)
+      const int bytes = __builtin_amdgcn_readfirstlane(n > 0 ? (n - 1) * (kDc * 2) + kR * 2 : 0);
+      return buf_rsrc(reinterpret_cast<const void*>(h | a), bytes);
     };
     u32x4_t rope[kRpw / 8];
     auto load_rope = [&](uint64_t addr) {
@@ -337,7 +339,7 @@ void decode_attn_kernel(DecodeArgs p) {
       constexpr int kQr = kRows / NW;                            // rows a wave loads
       const int q_row = wave * kQr;
       const int64_t first_row = static_cast<int64_t>(sq.q0) * p.nh + rt * kRows;
-      const int n_valid = clamp_int(n_rows - rt * kRows - q_row, 0, kQr);
+      const int n_valid = __builtin_amdgcn_readfirstlane(clamp_int(n_rows - rt * kRows - q_row, 0, kQr));
       const __amdgpu_buffer_rsrc_t rs = buf_rsrc(p.q_lat + (first_row + q_row) * kR, n_valid * kR * 2);
 #pragma unroll
       for (int i = 0; i < kQr; ++i)
