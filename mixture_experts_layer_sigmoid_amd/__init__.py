@@ -27,4 +27,4 @@ from ._lib import (  # noqa: F401
 )
 from .layer import (MoEForward, MoEBackward, RouterBackward, ExpertWeights, bias_update,  # noqa: F401
                     quantize_mx, quantize_mx_t, FMT)
-from .mla import LatentAttention, LatentDecode, latent_cache_append  # noqa: F401
+from .mla import LatentAttention, LatentDecode, LatentExpand, latent_cache_append  # noqa: F401

@@ -4,6 +4,8 @@ LatentAttention  expanded form: packed sequences of queries over expanded
                  keys and values (prompts, training), forward and backward.
 LatentDecode     absorbed form over a paged cache (serving): the last tokens
                  of each request, or a tree of drafted ones.
+LatentExpand     keys and values of all heads from latents, for the expanded
+                 form (one dense expert GEMM).
 latent_cache_append
                  RMS norm of new latents, rotary embedding of their keys and
                  of the queries, rows into the cache.
@@ -101,6 +103,28 @@ class LatentAttention:
                            cu_q, cu_k, B, self.Tq, self.Tk, h, self.causal, self.scale, self.dq, h * QK, self.dkv,
                            h * (NOPE + VALUE), self.dk_rope, ROPE, self.ws, stream)
         return self.dq, self.dkv, self.dk_rope
+
+
+class LatentExpand:
+    """kv = latents W_kvb^T for up to max_tokens latents: [T, 512] ->
+    [T, n_heads, 256] (each head's key part, then its value), as one
+    moe_grouped_fc2 call with a single expert. w_kvb [n_heads, 256, 512] bf16
+    is packed once here."""
+
+    def __init__(self, w_kvb, *, max_tokens):
+        self.n_heads, self.max_tokens = w_kvb.shape[0], max_tokens
+        self.w, _ = pack_weights(w_kvb.reshape(1, -1, LATENT).contiguous(), None, "bf16")
+        self.out = torch.empty((max_tokens, self.n_heads, NOPE + VALUE), dtype=torch.bfloat16, device=w_kvb.device)
+        self.offsets = torch.tensor([0, max_tokens], dtype=torch.int32, device=w_kvb.device)
+
+    def __call__(self, latents, stream=None):
+        """latents [max_tokens, 512] bf16, contiguous. Returns the object's
+        buffer [max_tokens, n_heads, 256]."""
+        _vec(latents, "latents", torch.bfloat16, (self.max_tokens, LATENT))
+        H = self.n_heads * (NOPE + VALUE)
+        L.moe_grouped_fc2(latents, None, L.MOE_BF16, self.w, None, L.MOE_BF16, self.offsets, 1, H, LATENT,
+                          self.max_tokens, self.out, L.MOE_BF16, stream)
+        return self.out
 
 
 class LatentDecode:

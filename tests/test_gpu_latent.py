@@ -466,3 +466,35 @@ def test_class_refusals(gpu_lib):
         args = {"kv_a": rows, "cache": pg.cache, "slots": slots} | kw
         with pytest.raises(ValueError):
             moe.latent_cache_append(args.pop("kv_a"), args.pop("cache"), args.pop("slots"), **args)
+
+
+def test_expand_is_the_projection(gpu_lib):
+    log("latent expand")
+    g = np.random.default_rng(4)
+    c, w = _bf(g.standard_normal((77, 512))), _bf(g.standard_normal((3, 256, 512)) / 512 ** 0.5)
+    kv = moe.LatentExpand(w, max_tokens=77)(c)
+    torch.cuda.synchronize()
+    want = np.einsum("tr,hdr->thd", _np(c), _np(w))
+    # exact products summed in fp32, one rounding
+    tol = ol.U * np.abs(want) + 2.0 ** -18 * np.einsum("tr,hdr->thd", np.abs(_np(c)), np.abs(_np(w)))
+    _inside(_np(kv), want, tol, "expand")
+
+
+def test_layer_example(gpu_lib):
+    """The example layer: prompt, decode steps, a drafted tree, gradients."""
+    log("latent layer example")
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "latent_moe_layer.py")
+    spec = importlib.util.spec_from_file_location("latent_moe_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    worst, tree, grads, y = mod.main(heads=16, hidden=512, prompt=130, steps=3)
+    torch.cuda.synchronize()
+    # expanded: kv and the weights rounded; absorbed: q_lat and the weights
+    # rounded; both outputs rounded. Relative to the output's norm each counts
+    # at most u = 2^-8 in the root mean square (a rounding's is below u / 1.7).
+    assert worst < 6 * 2.0 ** -8
+    # the same rows under other tiles: weights and result rounded on each side
+    assert tree < 4 * 2.0 ** -8
+    assert all(torch.isfinite(t.float()).all() for t in grads) and torch.isfinite(y.float()).all()
