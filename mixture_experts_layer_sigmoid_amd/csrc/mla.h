@@ -162,6 +162,24 @@ __device__ __forceinline__ float other_half(float v) {
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// ---- results --------------------------------------------------------------------
+// A wave's 32 result rows of RB bytes leave through LDS (`rows`, its own 32 x
+// (RB + 16) bytes): out of the registers a store would touch 32 rows with 8
+// bytes each, from here it writes whole rows.
+template <int RB>
+constexpr int result_bytes() { return 32 * (RB + 16); }
+template <int RB>
+__device__ __forceinline__ void store_rows(const uint8_t* rows, void* dst, int64_t ld_bytes, int n, int lane) {
+  constexpr int kC = RB / 16;                            // 16-byte pieces a row
+#pragma unroll
+  for (int i = 0; i < 32 * kC / 64; ++i) {
+    const int c = i * 64 + lane, r = c / kC;
+    if (r < n)
+      *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(dst) + r * ld_bytes + (c % kC) * 16) =
+          *reinterpret_cast<const u32x4_t*>(rows + r * (RB + 16) + (c % kC) * 16);
+  }
+}
+
 // ---- packed sequences --------------------------------------------------------
 // Sequence and tile of a work index: sequence b has ceil(n_b / per) tiles,
 // n_b = cu[b + 1] - cu[b]; all 64 lanes of the wave take part. Offsets are
@@ -170,18 +188,23 @@ struct SeqTile {
   int b;         // -1: no such tile
   int tile;      // within the sequence
   int start, n;  // the sequence's rows
+  int start2, n2;  // and those of the other side (keys for queries, queries for keys)
 };
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-__device__ __forceinline__ SeqTile find_tile(const int32_t* cu, int B, int total, int per, int index) {
+__device__ __forceinline__ SeqTile find_tile(const int32_t* cu, const int32_t* cu2, int B, int total, int total2,
+                                             int per, int index) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int b0 = 0; b0 < B; b0 += 64) {
     const int b = b0 + lane;
-    int s = 0, n = 0;
-    if (b < B) {
-      s = clamp_int(cu[b], 0, total);
-      n = clamp_int(cu[b + 1], s, total) - s;
+    int s = 0, n = 0, s2 = 0, n2 = 0;
+    if (b < B) {                       // both sides at once: one trip to memory
+      const int a0 = cu[b], a1 = cu[b + 1], b0_ = cu2[b], b1 = cu2[b + 1];
+      s = clamp_int(a0, 0, total);
+      n = clamp_int(a1, s, total) - s;
+      s2 = clamp_int(b0_, 0, total2);
+      n2 = clamp_int(b1, s2, total2) - s2;
     }
     const int tiles = (n + per - 1) / per;
     int sum = tiles;
@@ -198,11 +221,13 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* cu, int B, int total
       t.tile = index - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(tiles, l));
       t.start = __builtin_amdgcn_readlane(s, l);
       t.n = __builtin_amdgcn_readlane(n, l);
+      t.start2 = __builtin_amdgcn_readlane(s2, l);
+      t.n2 = __builtin_amdgcn_readlane(n2, l);
       return t;
     }
     before += __builtin_amdgcn_readlane(sum, 63);
   }
-  return SeqTile{-1, 0, 0, 0};
+  return SeqTile{-1, 0, 0, 0, 0, 0};
 }
 
 // Workgroups go to the XCDs round-robin; give each XCD a contiguous run of

@@ -120,11 +120,10 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int idx, uint8_t* smem)
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int head = idx / p.k_tiles;
-  const SeqTile st = find_tile(p.cu_k, p.B, p.Tk, kKvKeys, idx % p.k_tiles);
+  const SeqTile st = find_tile(p.cu_k, p.cu_q, p.B, p.Tk, p.Tq, kKvKeys, idx % p.k_tiles);
   if (st.b < 0) return;
   const int n_k = st.n;
-  const int q_start = clamp_int(p.cu_q[st.b], 0, p.Tq);
-  const int n_q = clamp_int(p.cu_q[st.b + 1], q_start, p.Tq) - q_start;
+  const int q_start = st.start2, n_q = st.n2;
   const int k0 = st.tile * kKvKeys;
   const int key = k0 + wave * 32 + (lane & 31);
   const int keyc = key < n_k ? key : n_k - 1;
@@ -279,25 +278,32 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int idx, uint8_t* smem)
   for (; t < cut_end; ++t) tile(t, std::true_type{});
   for (; t < t_end; ++t) tile(t, std::false_type{});
   acc_settled();
-  if (key >= n_k) return;
-  const int64_t tok = static_cast<int64_t>(st.start) + key;
-  uint16_t* o = p.dkv + tok * p.dkv_ld + head * (kDn + kDv) + 4 * g;
+  lds_barrier();                        // everyone is done with the tiles
   auto value = [&](const f32x16_t& v, int i) {
     return f32x4_t{read_acc(v[4 * i]), read_acc(v[4 * i + 1]), read_acc(v[4 * i + 2]), read_acc(v[4 * i + 3])};
   };
+  constexpr int kRb = (kDn + kDv) * 2;
+  static_assert(kKvWaves * result_bytes<kRb>() <= 2 * kLdsKvStage, "results fit the tile buffers");
+  uint8_t* rows = smem + wave * result_bytes<kRb>();
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4_t x = value(dk[c], i) * p.scale, y = value(dv[c], i);
-      *reinterpret_cast<uint2*>(o + 32 * c + 8 * i) = pack4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<uint2*>(o + kDn + 32 * c + 8 * i) = pack4(y[0], y[1], y[2], y[3]);
+      uint8_t* o = rows + (lane & 31) * (kRb + 16) + (32 * c + 8 * i + 4 * g) * 2;
+      *reinterpret_cast<uint2*>(o) = pack4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint2*>(o + kDn * 2) = pack4(y[0], y[1], y[2], y[3]);
     }
-  float* r = p.dkr_part + (static_cast<int64_t>(head) * p.Tk + tok) * kDr + 4 * g;
+  const int64_t tok = static_cast<int64_t>(st.start) + k0 + wave * 32;
+  const int n_out = n_k - k0 - wave * 32;
+  store_rows<kRb>(rows, p.dkv + tok * p.dkv_ld + head * (kDn + kDv), p.dkv_ld * 2, n_out, lane);
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4_t*>(r + 32 * c + 8 * i) = value(dk[4 + c], i);
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<f32x4_t*>(rows + (lane & 31) * (kDr * 4 + 16) + (32 * c + 8 * i + 4 * g) * 4) =
+          value(dk[4 + c], i);
+  store_rows<kDr * 4>(rows, p.dkr_part + (static_cast<int64_t>(head) * p.Tk + tok) * kDr, kDr * 4, n_out, lane);
 }
 
 // ---- dq: a wave keeps 32 queries (the lanes' columns), keys pass by ----------
@@ -311,10 +317,9 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int idx, uint8_t* smem) 
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int head = idx / p.q_tiles;
-  const SeqTile st = find_tile(p.cu_q, p.B, p.Tq, kQRows, p.q_tiles - 1 - idx % p.q_tiles);
+  const SeqTile st = find_tile(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, kQRows, p.q_tiles - 1 - idx % p.q_tiles);
   if (st.b < 0) return;
-  const int k_start = clamp_int(p.cu_k[st.b], 0, p.Tk);
-  const int n_k = clamp_int(p.cu_k[st.b + 1], k_start, p.Tk) - k_start;
+  const int k_start = st.start2, n_k = st.n2;
   const int n_q = st.n;
   const int q0 = st.tile * kQRows;
   const int row = q0 + wave * 32 + (lane & 31);
@@ -422,17 +427,19 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int idx, uint8_t* smem) 
   for (; kt < n_kt; ++kt) tile(kt, std::true_type{});
 
   acc_settled();
-  if (row >= n_q) return;
-  uint16_t* o = p.dq + tokc * p.dq_ld + head * kDq + 4 * g;
+  lds_barrier();                        // everyone is done with the tiles
+  uint8_t* rows = smem + wave * result_bytes<kDq * 2>();
 #pragma unroll
   for (int c = 0; c < 6; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float sc = p.scale;
-      *reinterpret_cast<uint2*>(o + 32 * c + 8 * i) =
+      *reinterpret_cast<uint2*>(rows + (lane & 31) * (kDq * 2 + 16) + (32 * c + 8 * i + 4 * g) * 2) =
           pack4(read_acc(dq[c][4 * i]) * sc, read_acc(dq[c][4 * i + 1]) * sc, read_acc(dq[c][4 * i + 2]) * sc,
                 read_acc(dq[c][4 * i + 3]) * sc);
     }
+  const int64_t tok = static_cast<int64_t>(st.start) + q0 + wave * 32;
+  store_rows<kDq * 2>(rows, p.dq + tok * p.dq_ld + head * kDq, p.dq_ld * 2, n_q - q0 - wave * 32, lane);
 }
 
 // Both parts in one launch, dk / dv first: the second fills the compute units

@@ -44,10 +44,9 @@ void attn_fwd_kernel(FwdArgs p) {
   const int idx = xcd_contiguous(blockIdx.x, gridDim.x);
   const int head = idx / p.n_tiles;
   // later tiles of a sequence see more keys: longest first
-  const SeqTile st = find_tile(p.cu_q, p.B, p.Tq, kQt, p.n_tiles - 1 - idx % p.n_tiles);
+  const SeqTile st = find_tile(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, kQt, p.n_tiles - 1 - idx % p.n_tiles);
   if (st.b < 0) return;
-  const int k_start = clamp_int(p.cu_k[st.b], 0, p.Tk);
-  const int n_k = clamp_int(p.cu_k[st.b + 1], k_start, p.Tk) - k_start;
+  const int k_start = st.start2, n_k = st.n2;
   const int n_q = st.n;
 
   const int row = st.tile * kQt + wave * 32 + (lane & 31);       // within the sequence
@@ -159,18 +158,19 @@ void attn_fwd_kernel(FwdArgs p) {
       }
   }
   l += other_half(l);
-  if (row >= n_q) return;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  const int64_t tok = static_cast<int64_t>(st.start) + row;
-  uint16_t* out = p.out + tok * p.out_ld + head * kDv + 4 * g;
+  lds_barrier();                        // everyone is done with the tiles
+  uint8_t* rows = smem + wave * result_bytes<kDv * 2>();
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint2*>(out + 32 * c + 8 * i) =
+      *reinterpret_cast<uint2*>(rows + (lane & 31) * (kDv * 2 + 16) + (32 * c + 8 * i + 4 * g) * 2) =
           pack4(o[c][4 * i] * inv, o[c][4 * i + 1] * inv, o[c][4 * i + 2] * inv, o[c][4 * i + 3] * inv);
-  if (p.lse && g == 0)
-    p.lse[tok * p.nh + head] = l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
+  const int64_t tok = static_cast<int64_t>(st.start) + st.tile * kQt + wave * 32;
+  store_rows<kDv * 2>(rows, p.out + tok * p.out_ld + head * kDv, p.out_ld * 2, n_q - st.tile * kQt - wave * 32, lane);
+  if (p.lse && g == 0 && row < n_q)
+    p.lse[(tok + lane) * p.nh + head] = l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
 }
 
 }  // namespace
