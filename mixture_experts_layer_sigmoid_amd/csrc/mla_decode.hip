@@ -11,6 +11,24 @@
 // Three launches: the products with W_UK; the attention, its work cut evenly
 // over the chip along the cached tokens; the joining of the pieces with the
 // products with W_UV.
+//
+// Roundings: q_lat to bf16 and the weights p to bf16 (both operands of matrix
+// instructions, rms 2^-9.2 of each; a wider q_lat would double the products
+// of the scores); o_lat stays fp32 up to W_UV, where it enters as two bf16
+// terms. Scores, references, sums and pieces are fp32. Against 64 bits out has
+// 1.8e-3 to 2.5e-3 rms, 1.66e-3 of it the output's own rounding; q_lat's shows
+// most where a row has few keys.
+//
+// Bound, by size (an 8192^3 bf16 product reaches 1369 TFLOP/s here, a copy
+// 4.87 TB/s):
+//   256 tokens of 8 trees x 128 heads: 291 us attention = 740 TFLOP/s, operands
+//     through LDS (a value operand serves two row blocks; matrix unit 39% busy);
+//   64 ragged requests x 128 heads: 82 us, of it the pieces' starts and ends
+//     (queries in, sums out: about 18k cycles a piece against 4.9k a tile of 64
+//     tokens and 64 rows); join 20, q_lat 9.5 us;
+//   8 long caches x 16 heads, 279k cached tokens: 63 us = 5.1 TB/s, at the
+//     rate of a copy; join 14.5 us (its pieces' traffic);
+//   one request x 16 heads, 531 tokens: 2.9 + 10.0 + 6.7 us, latency.
 #include "mla.h"
 
 #include <cmath>
@@ -22,7 +40,7 @@ namespace {
 constexpr int kTok = 64;                               // cached tokens per tile
 constexpr int kLat = kTok * kR * 2, kRope = kTok * kDr * 2, kTile = kLat + kRope;
 constexpr int kAhead = 6;                              // matrix operands read ahead
-constexpr int kPieceCost = 4;
+constexpr int kPieceCost = 4;                          // in token tiles; see the work list
 constexpr int kGroups = 256;                           // workgroups of the attention
 
 struct DecodeArgs {
@@ -112,7 +130,9 @@ __global__ __launch_bounds__(256) void absorb_kernel(DecodeArgs p) {
 // kPieceCost + its token tiles long (a group's start and end cost about as
 // much as four tiles: queries in, sums out), and the whole is cut into equal
 // runs, one for each team. A run's piece of a group is the token tiles in it;
-// the part of a run in front of them stands for no work.
+// the part of a run in front of them stands for no work. kPieceCost 0 / 4 / 8:
+// 64 ragged requests x 128 heads 95 / 82 / 87 us, long caches x 16 heads 77 /
+// 63 / 63, trees of 32 x 128 heads 306 / 291 / 289.
 struct Seq {
   int q0, nq, len, tok_tiles, units;
 };
@@ -207,7 +227,8 @@ __device__ __forceinline__ void scale_operand(bf16x8_t& v, float f) {
 // moved, both are brought to the larger before the product.
 constexpr int kXchg = 64 * 32;                        // bytes of one wave's weights
 // kRun: every run of kRpw token rows that a wave loads lies in one page, and
-// takes one buffer resource (any other page size: one a row).
+// takes one buffer resource (any other page size: one a row, which costs the
+// trees of 32 x 128 heads 299 us instead of 291).
 template <int WR, bool kRun>
 __global__ __launch_bounds__(128 * WR) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void decode_attn_kernel(DecodeArgs p) {
@@ -744,7 +765,10 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs p, int rows
 }
 
 constexpr int kJoinTok = 32;
-// tokens of a joining workgroup: as many as leave two workgroups a compute unit
+// Tokens of a joining workgroup: more share a head's matrix, fewer join more
+// pieces at once. As many as leave two workgroups a compute unit; always 32:
+// 12 instead of 6.7 us (1 token x 16 heads), 44 instead of 9 (21), 77 instead
+// of 14.5 (8 long caches); at most 16: 47 instead of 41 (256 x 128 heads).
 int join_tokens(int T, int nh) {
   int n = kJoinTok;
   while (n > 1 && static_cast<int64_t>((T + n - 1) / n) * nh < 2 * kNumCu) n /= 2;
@@ -753,7 +777,8 @@ int join_tokens(int T, int nh) {
 
 // Row tiles taken in step by as many workgroups: the largest power of two (at
 // most the 32 workgroups of an XCD) that leaves no more than a sixth of the
-// places empty for a request of average size.
+// places empty for a request of average size. Each by itself: 336 instead of
+// 291 us (trees of 32 x 128 heads), 85 instead of 82 (one token x 128 heads).
 int team_size(int64_t T, int B, int nh, int rows) {
   const int64_t tiles = ((T * nh + B - 1) / B + rows - 1) / rows;
   int n = kGroups / kNumXcd;
@@ -761,7 +786,10 @@ int team_size(int64_t T, int B, int nh, int rows) {
   return n;
 }
 
-// rows of a row tile: by the new rows a request brings on average
+// Rows of a row tile, by the new rows a request brings on average. 32 where
+// 64 are taken: 121 instead of 82 us (one token x 128 heads), 485 instead of
+// 291 (32 x 128), the same at 7 x 16; 64 where 32 are taken: 11.3 instead of
+// 10.0 (one token x 16 heads), 67 instead of 63 (long caches).
 int tile_rows(int64_t T, int B, int nh) {
   const int64_t avg = (T * nh + B - 1) / B;
   return avg <= 32 ? 32 : 64;
