@@ -41,6 +41,7 @@ constexpr int kTok = 64;                               // cached tokens per tile
 constexpr int kLat = kTok * kR * 2, kRope = kTok * kDr * 2, kTile = kLat + kRope;
 constexpr int kAhead = 6;                              // matrix operands read ahead
 constexpr int kPieceCost = 4;                          // in token tiles; see the work list
+constexpr int kShortRuns = 96;                         // more units: runs of two and more
 constexpr int kGroups = 256;                           // workgroups of the attention
 
 struct DecodeArgs {
@@ -141,6 +142,11 @@ __global__ __launch_bounds__(256) void absorb_kernel(DecodeArgs p) {
 // the part of a run in front of them stands for no work. kPieceCost 0 / 4 / 8:
 // 64 ragged requests x 128 heads 95 / 82 / 87 us, long caches x 16 heads 77 /
 // 63 / 63, trees of 32 x 128 heads 306 / 291 / 289.
+// Little work is not cut to single tiles once there are more than kShortRuns
+// units, as every piece is another one to join. Runs of one / two / three
+// units, attention and join together: 136 units (7 tokens x 8 heads, 8404
+// cached) 35.8 / 30.1 / 29.6 us, 63 units (7 x 16, 3 requests) 26.5 / 28.5 /
+// 31, 13 units (1 x 16) 17.1 / 18.7 / 19.9.
 struct Seq {
   int q0, nq, len, tok_tiles, units;
 };
@@ -254,7 +260,7 @@ void decode_attn_kernel(DecodeArgs p) {
   const SeqBlock seqs = load_block(p, 0, kRows);
   const int total = total_units(p, kRows, seqs);
   const int teams = kGroups / p.team;
-  const int per = (total + teams - 1) / teams;
+  const int per = max(total > kShortRuns ? 2 : 1, (total + teams - 1) / teams);
   const int grp = xcd_contiguous(blockIdx.x, kGroups);
   const int my_team = grp / p.team, member = grp % p.team;
   int u = my_team * per;
