@@ -272,6 +272,18 @@ def test_decode_many_requests_and_long_ones(gpu_lib):
     _check_decode(pg, q, [1] * 130, out, lse, what="many")
 
 
+@pytest.mark.parametrize("lens", [[5888], [5889], [6337, 1]])
+def test_decode_runs_of_one_and_of_two_tiles(gpu_lib, lens):
+    """Where the cut changes: 92 token tiles (runs of one), 93 and 100 (runs of two, the last of one)."""
+    log(f"latent decode runs {lens}")
+    nq = [2] + [1] * (len(lens) - 1)
+    pg = Paged(5, lens, 32, 3)
+    q = _draw(5, [sum(nq)], [1], 3)[0]
+    out, lse = _decode(pg, q, nq)
+    torch.cuda.synchronize()
+    _check_decode(pg, q, nq, out, lse, what="runs")
+
+
 @pytest.mark.parametrize("h,nq,lens", [(16, 7, [100, 7, 64]), (4, 48, [48, 75]), (128, 5, [61])])
 def test_decode_trees(gpu_lib, h, nq, lens):
     log(f"latent tree h={h} nq={nq}")
