@@ -49,6 +49,12 @@ def _vec(t: torch.Tensor, name: str, dtype, shape: tuple) -> torch.Tensor:
     return t
 
 
+def _cache(t: torch.Tensor, what: str) -> None:
+    if t.dtype is not torch.bfloat16 or t.shape[-1] != CACHE_ROW or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"cache must be a contiguous bfloat16 tensor {what} on the GPU, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 class LatentAttention:
     """Attention of up to Tq queries over up to Tk expanded keys in up to
     n_seqs packed sequences (cu_q, cu_k [n_seqs + 1] int32, row offsets).
@@ -155,9 +161,9 @@ class LatentDecode:
         T, B, h = q.shape[0], lens.shape[0], self.n_heads
         if T > self.max_tokens or B > self.max_seqs:
             raise ValueError(f"at most {self.max_tokens} tokens of {self.max_seqs} requests")
-        if cache.dtype != torch.bfloat16 or cache.dim() != 3 or cache.shape[2] != CACHE_ROW or \
-                not cache.is_contiguous():
-            raise ValueError("cache must be a contiguous bfloat16 tensor [n_pages, page_size, 576]")
+        if cache.dim() != 3:
+            raise ValueError("cache must have three dimensions [n_pages, page_size, 576]")
+        _cache(cache, "[n_pages, page_size, 576]")
         _vec(page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
         _vec(lens, "lens", torch.int32, (B,))
         _vec(cu_q, "cu_q", torch.int32, (B + 1,))
@@ -179,8 +185,7 @@ def latent_cache_append(kv_a, cache, slots, *, norm_weight=None, eps=1e-6, cos=N
     part, into q_out (in place without q_out). cos, sin [max_pos, 32] fp32,
     positions [T] int32. Returns q_out."""
     T = kv_a.shape[0]
-    if cache.dtype != torch.bfloat16 or cache.shape[-1] != CACHE_ROW or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous bfloat16 tensor [..., 576]")
+    _cache(cache, "[..., 576]")
     kv_ld = _rows(kv_a, "kv_a", (CACHE_ROW,))
     _vec(slots, "slots", torch.int64, (T,))
     if norm_weight is not None:
