@@ -55,6 +55,12 @@ def _cache(t: torch.Tensor, what: str) -> None:
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _weights(t: torch.Tensor) -> None:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (NOPE + VALUE, LATENT) or not t.is_cuda:
+        raise ValueError(f"w_kvb must be a bfloat16 tensor [n_heads, {NOPE + VALUE}, {LATENT}] on the GPU, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 class LatentAttention:
     """Attention of up to Tq queries over up to Tk expanded keys in up to
     n_seqs packed sequences (cu_q, cu_k [n_seqs + 1] int32, row offsets).
@@ -118,6 +124,7 @@ class LatentExpand:
     is packed once here."""
 
     def __init__(self, w_kvb, *, max_tokens):
+        _weights(w_kvb)
         self.n_heads, self.max_tokens = w_kvb.shape[0], max_tokens
         self.w, _ = pack_weights(w_kvb.reshape(1, -1, LATENT).contiguous(), None, "bf16")
         self.out = torch.empty((max_tokens, self.n_heads, NOPE + VALUE), dtype=torch.bfloat16, device=w_kvb.device)
@@ -139,9 +146,8 @@ class LatentDecode:
     head's W_UK rows, then its W_UV rows (bf16); packed once here."""
 
     def __init__(self, w_kvb, *, max_tokens, max_seqs, scale=SCALE):
+        _weights(w_kvb)
         h = w_kvb.shape[0]
-        if w_kvb.dtype != torch.bfloat16 or tuple(w_kvb.shape[1:]) != (NOPE + VALUE, LATENT):
-            raise ValueError("w_kvb must be a bfloat16 tensor [n_heads, 256, 512]")
         self.n_heads, self.max_tokens, self.max_seqs, self.scale = h, max_tokens, max_seqs, scale
         self.w_uk, _ = pack_weights(w_kvb[:, :NOPE].transpose(1, 2).contiguous(), None, "bf16")
         self.w_uv, _ = pack_weights(w_kvb[:, NOPE:].contiguous(), None, "bf16")

@@ -35,3 +35,15 @@ def test_append_refuses_a_cache_in_host_memory(no_calls):
     cache = torch.zeros((3, 16, 576), dtype=BF)
     with pytest.raises(ValueError, match="cache"):
         mla.latent_cache_append(torch.zeros((1, 576), dtype=BF), cache, torch.zeros(1, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("shape,dtype", [((2, 128, 512), BF), ((2, 256, 512), torch.float32),
+                                         ((2, 256, 512), torch.float16), ((2, 256, 576), BF), ((256, 512), BF),
+                                         ((2, 256, 512), BF)])
+def test_weights_are_refused_before_packing(no_calls, shape, dtype):
+    """Another shape or type, and the right ones in host memory."""
+    w = torch.zeros(shape, dtype=dtype)
+    with pytest.raises(ValueError, match="w_kvb"):
+        mla.LatentExpand(w, max_tokens=4)
+    with pytest.raises(ValueError, match="w_kvb"):
+        mla.LatentDecode(w, max_tokens=4, max_seqs=1)
