@@ -133,3 +133,94 @@ def cache_row(kv_a, w, eps):
     """Normalized latents of rows [T, >= 512]."""
     c = kv_a[:, :LATENT]
     return c / np.sqrt((c * c).mean(1, keepdims=True) + eps) * w
+
+
+# ---- root mean squares of the errors ------------------------------------------
+# The bounds above hold for every element, and so are wide where many terms
+# add up. The errors of the roundings are independent and of mean zero, each at
+# most uniform over half a unit in the last place (root mean square
+# U / sqrt(3) of the value, just above a power of two), so what they do to a
+# row of results has a root mean square that the functions below give.
+RMS = U / 3 ** 0.5
+
+
+def _norm(var):
+    return np.sqrt(var.sum(-1))
+
+
+def cached_spread(q, w_kvb, rows, scale, tree=None):
+    """cached()'s out and lse, with the root mean square of the error of each
+    (token, head): the norm of out's 128 values (out_rms), lse (lse_rms). The
+    absorbed query and the result are rounded once each, the weights at most
+    twice (again where the two halves of a tile had other references). fp32 is
+    out_floor and lse_floor, bounds and not root mean squares: scores are off
+    by 2^-22 of their terms' absolute values, sums by 2^-20 of theirs."""
+    n_q, h = q.shape[:2]
+    n = rows.shape[0]
+    first = n - n_q
+    res = {"out": np.zeros((n_q, h, VALUE)), "lse": np.full((n_q, h), -np.inf), "out_rms": np.zeros((n_q, h)),
+           "lse_rms": np.zeros((n_q, h)), "out_floor": np.zeros((n_q, h)), "lse_floor": np.zeros((n_q, h))}
+    wk, wv = w_kvb[:, :NOPE], w_kvb[:, NOPE:]
+    with np.errstate(invalid="ignore"):
+        values = np.matmul(rows[None, :, :LATENT], wv.transpose(0, 2, 1))            # [h, n, 128]
+    for i in range(n_q):
+        new = np.arange(n) - first
+        if tree is None:
+            see = new <= i
+        else:
+            word = int(tree[i])
+            see = np.array([v < 0 or (v < 64 and bool((word >> v) & 1)) for v in new.tolist()], bool)
+        if not see.any():
+            continue
+        c, v = rows[see], values[:, see]
+        ql = np.matmul(q[i, :, None, :NOPE], wk)[:, 0]                               # [h, 512]
+        p, lse = softmax(scale * (ql @ c[:, :LATENT].T + q[i, :, NOPE:] @ c[:, LATENT:].T), True)
+        out = np.matmul(p[:, None], v)[:, 0]
+        # a score moves by scale q_r c_r times the error of q_lat's element r
+        moved = np.matmul(c[:, :LATENT].T[None], p[..., None] * (v - out[:, None]))  # [h, 512, 128]
+        var = (RMS * out) ** 2 + 2 * RMS ** 2 * np.matmul((p * p)[:, None], v * v)[:, 0]
+        var += (scale * RMS) ** 2 * np.matmul((ql * ql)[:, None], moved * moved)[:, 0]
+        res["out"][i], res["lse"][i], res["out_rms"][i] = out, lse, _norm(var)
+        res["lse_rms"][i] = scale * RMS * _norm((ql * (p @ c[:, :LATENT])) ** 2)
+        mass = np.matmul(np.abs(wv), (p @ np.abs(c[:, :LATENT]))[..., None])[..., 0]
+        terms = np.abs(ql) @ np.abs(c[:, :LATENT]).T + np.abs(q[i, :, NOPE:]) @ np.abs(c[:, LATENT:]).T
+        off = 2.0 ** -22 * scale * terms.max(1)
+        res["out_floor"][i] = (2.0 ** -20 + 2 * off) * _norm(mass ** 2)
+        res["lse_floor"][i] = off + 2.0 ** -20 * (1 + np.abs(lse))
+    return res
+
+
+def attention_spread(dout, q, kv, k_rope, causal, scale):
+    """attention() and attention_backward(), with the root mean square of the
+    error of each row of a head: out and dq (norms over a query's values), dk
+    and dv (the two halves of a key's dkv), dk_rope (over the heads' sum). The
+    weights, ds and the results are rounded once each; delta is formed from
+    the rounded output of rounded weights."""
+    n_q, h = q.shape[:2]
+    n_k = kv.shape[0]
+    see = visible(n_q, n_k, causal)
+    r = {"out": np.zeros((n_q, h, VALUE)), "dq": np.zeros(q.shape), "dkv": np.zeros(kv.shape),
+         "dk_rope": np.zeros(k_rope.shape)}
+    rms = {"out_rms": np.zeros((n_q, h)), "dq_rms": np.zeros((n_q, h)), "dk_rms": np.zeros((n_k, h)),
+           "dv_rms": np.zeros((n_k, h))}
+    rope_var = np.zeros(k_rope.shape)
+    for x in range(h):
+        k = np.concatenate([kv[:, x, :NOPE], k_rope], 1)
+        v, do, qx = kv[:, x, NOPE:], dout[:, x], q[:, x]
+        p, _ = softmax(scale * (qx @ k.T), see)
+        o = p @ v
+        dp = do @ v.T
+        ds = p * (dp - (p * dp).sum(1, keepdims=True))
+        dq, dk, dv = scale * (ds @ k), scale * (ds.T @ qx), p.T @ do
+        r["out"][:, x], r["dq"][:, x], r["dkv"][:, x] = o, dq, np.concatenate([dk[:, :NOPE], dv], 1)
+        r["dk_rope"] += dk[:, NOPE:]
+        o_var = RMS ** 2 * ((p * p) @ (v * v) + o * o)
+        delta_var = (do * do * o_var).sum(1, keepdims=True)                 # one error a query, for all its keys
+        ds_var = RMS ** 2 * ds * ds
+        dk_var = scale ** 2 * ((ds_var + p * p * delta_var).T @ (qx * qx))
+        rms["out_rms"][:, x] = _norm(o_var)
+        rms["dq_rms"][:, x] = _norm(scale ** 2 * (ds_var @ (k * k) + delta_var * (p @ k) ** 2) + (RMS * dq) ** 2)
+        rms["dk_rms"][:, x] = _norm(dk_var[:, :NOPE] + (RMS * dk[:, :NOPE]) ** 2)
+        rms["dv_rms"][:, x] = _norm(RMS ** 2 * ((p * p).T @ (do * do) + dv * dv))
+        rope_var += dk_var[:, NOPE:]
+    return {**r, **rms, "dk_rope_rms": _norm(rope_var + (RMS * r["dk_rope"]) ** 2)}
