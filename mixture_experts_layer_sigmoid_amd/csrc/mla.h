@@ -252,7 +252,8 @@ inline int check_expanded(const std::string& fn, int fmt, int B, int Tq, int Tk,
   MOE_REQUIRE(B >= 0 && Tq >= 0 && Tk >= 0 && Tq <= (1 << 28) && Tk <= (1 << 28), MOE_ERR_INVALID_ARG,
               fn + ": B must be >= 0, Tq and Tk in [0, 2^28]");
   MOE_REQUIRE(nh >= 1 && nh <= 1024, MOE_ERR_INVALID_ARG, fn + ": n_heads must be in [1, 1024]");
-  // grids stay below 2^32 work items
+  // grids stay below 2^32 work items (the backward's sums of the heads' rotary
+  // gradients, 64 work items a key, are cut into launches that do)
   MOE_REQUIRE(static_cast<int64_t>(Tq) * nh <= (1 << 27) && static_cast<int64_t>(Tk) * nh <= (1 << 27) &&
                   static_cast<int64_t>(B) * nh <= (1 << 22),
               MOE_ERR_INVALID_ARG, fn + ": Tq * n_heads and Tk * n_heads must be <= 2^27, B * n_heads <= 2^22");

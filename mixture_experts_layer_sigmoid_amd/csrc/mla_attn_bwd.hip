@@ -479,15 +479,18 @@ void bwd_kernel(BwdArgs p) {
 
 // ---- dk_rope[t] = scale * sum over heads, in head order ----------------------
 // A workgroup takes 4 tokens: 16 lanes x 4 values a token, 4 groups of heads
-// whose sums are joined in a fixed order. Only rows that a sequence holds.
-__global__ __launch_bounds__(256) void bwd_rope_kernel(BwdArgs p) {
+// whose sums are joined in a fixed order. Only rows that a sequence holds;
+// `skip` is where this launch's part of them starts.
+constexpr int kRopeTok = 4;
+constexpr int kRopeLaunch = 1 << 25;   // tokens of one launch: 64 work items each, below 2^32
+__global__ __launch_bounds__(256) void bwd_rope_kernel(BwdArgs p, int skip) {
   __shared__ f32x4_t part[4][64];
   const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
   const int lo = clamp_int(p.cu_k[0], 0, p.Tk), hi = clamp_int(p.cu_k[p.B], lo, p.Tk);
-  const int t = lo + blockIdx.x * 4 + (lane >> 4);
+  const int64_t t = static_cast<int64_t>(lo) + skip + blockIdx.x * kRopeTok + (lane >> 4);
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
   if (t < hi) {
-    const float* src = p.dkr_part + static_cast<int64_t>(t) * kDr + (lane & 15) * 4;
+    const float* src = p.dkr_part + t * kDr + (lane & 15) * 4;
 #pragma unroll 8
     for (int h = grp; h < p.nh; h += 4) {
       const f32x4_t v = *reinterpret_cast<const f32x4_t*>(src + static_cast<int64_t>(h) * p.Tk * kDr);
@@ -502,7 +505,7 @@ __global__ __launch_bounds__(256) void bwd_rope_kernel(BwdArgs p) {
     for (int k = 1; k < 4; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] += part[k][lane][i];
-    *reinterpret_cast<uint2*>(p.dkr + static_cast<int64_t>(t) * p.dkr_ld + (lane & 15) * 4) =
+    *reinterpret_cast<uint2*>(p.dkr + t * p.dkr_ld + (lane & 15) * 4) =
         pack4(s[0] * p.scale, s[1] * p.scale, s[2] * p.scale, s[3] * p.scale);
   }
 }
@@ -561,6 +564,9 @@ extern "C" int moe_mla_attn_bwd(const void* dout, int64_t dout_ld, const void* q
   a.q_tiles = Tq > 0 ? seq_tiles_bound(B, Tq, kQRows) : 0;
   hipLaunchKernelGGL(bwd_kernel, dim3(static_cast<unsigned>(a.k_tiles + a.q_tiles) * n_heads), dim3(64 * kQWaves), 0,
                      stream, a);
-  if (Tk > 0) hipLaunchKernelGGL(bwd_rope_kernel, dim3((Tk + 3) / 4), dim3(256), 0, stream, a);
+  for (int skip = 0; skip < Tk; skip += kRopeLaunch) {
+    const int n = Tk - skip < kRopeLaunch ? Tk - skip : kRopeLaunch;
+    hipLaunchKernelGGL(bwd_rope_kernel, dim3((n + kRopeTok - 1) / kRopeTok), dim3(256), 0, stream, a, skip);
+  }
   return check_launch(fn);
 }
