@@ -3,10 +3,12 @@ more work items or workgroups than one launch may have."""
 import pytest
 import torch
 
+import mixture_experts_layer_sigmoid_amd as moe
 from mixture_experts_layer_sigmoid_amd import _lib as L
 from tests.gpu_util import log
-from tests.test_gpu_latent import SCALE, _draw, _i32
+from tests.test_gpu_latent import SCALE, Paged, _draw, _i32
 from tests.test_gpu_latent_gradients import check
+from tests.test_gpu_latent_rows import _check
 
 pytestmark = pytest.mark.gpu
 
@@ -35,4 +37,25 @@ def test_backward_of_more_than_2_to_26_keys(gpu_lib):
     for a in range(0, many, 1 << 24):
         assert not dkv[a:a + (1 << 24)].any()
     del kv, dkv, dkr, kr, ws
+    torch.cuda.empty_cache()
+
+
+def test_decode_of_2_to_24_tokens(gpu_lib):
+    """The most that a call takes with one head: 131072 blocks of 128 tokens,
+    524288 of 32; all but three of the tokens are in no request (70 GB)."""
+    log("latent decode of 2^24 tokens")
+    T, n = 1 << 24, 3
+    at = T - n - 2
+    pg = Paged(2, [90], 16, 1)
+    q = torch.empty((T, 1, 192), dtype=torch.bfloat16, device="cuda")
+    q[at:at + n] = _draw(7, [n], [1], 1)[0]
+    plan = moe.LatentDecode(pg.w, max_tokens=T, max_seqs=1)
+    plan.out.fill_(7.0)
+    lse = torch.full((T, 1), 7.0, device="cuda")
+    out = plan(q, pg.cache, _i32(pg.table), _i32(pg.lens), _i32([at, at + n]), lse=lse)
+    torch.cuda.synchronize()
+    _check(pg, q[at:at + n], [n], out[at:at + n], lse[at:at + n])
+    for t in (out, lse):
+        assert (t[:at] == 7).all() and (t[at + n:] == 7).all()
+    del plan, q, out, lse
     torch.cuda.empty_cache()
