@@ -36,7 +36,7 @@ def _rows(t: torch.Tensor, name: str, inner: tuple) -> int:
     if shape[1:] != inner:
         raise ValueError(f"{name} must have shape [tokens, {', '.join(map(str, inner))}], got {tuple(shape)}")
     last = inner[-1]
-    if stride[-1] != 1 or (len(inner) == 2 and stride[1] != last and inner[0] > 1):
+    if shape[0] > 0 and (stride[-1] != 1 or (len(inner) == 2 and stride[1] != last and inner[0] > 1)):
         raise ValueError(f"{name}: a token's values must be consecutive")
     # a lone token's stride is never used, and may be anything
     return stride[0] if shape[0] > 1 else last * (inner[0] if len(inner) == 2 else 1)

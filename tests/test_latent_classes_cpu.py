@@ -47,3 +47,18 @@ def test_weights_are_refused_before_packing(no_calls, shape, dtype):
         mla.LatentExpand(w, max_tokens=4)
     with pytest.raises(ValueError, match="w_kvb"):
         mla.LatentDecode(w, max_tokens=4, max_seqs=1)
+
+
+def test_rows_of_no_tokens_have_no_strides_to_check():
+    """numpy gives empty arrays strides of their own; there are no values."""
+    class Empty:
+        dtype, is_cuda = BF, True
+        shape = torch.Size((0, 3, 192))
+
+        def stride(self):
+            return (0, 0, 0)
+
+    assert mla._rows(Empty(), "q", (3, 192)) == 3 * 192
+    Empty.shape = torch.Size((1, 3, 192))
+    with pytest.raises(ValueError, match="consecutive"):
+        mla._rows(Empty(), "q", (3, 192))
