@@ -61,12 +61,18 @@ def _weights(t: torch.Tensor) -> None:
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _first(t: torch.Tensor, n: int) -> torch.Tensor:
+    """The first n rows of a buffer."""
+    return t if t.shape[0] == n else t[:n]
+
+
 class LatentAttention:
     """Attention of up to Tq queries over up to Tk expanded keys in up to
     n_seqs packed sequences (cu_q, cu_k [n_seqs + 1] int32, row offsets).
     With causal, a sequence's last query sees all its keys, each earlier one
-    a key less. Outputs live in the object's buffers; backward=True adds the
-    gradients' buffers and workspace."""
+    a key less. Outputs are views of the object's buffers, as many rows as the
+    call's inputs have; backward=True adds the gradients' buffers and
+    workspace."""
 
     def __init__(self, *, Tq, Tk, n_heads, n_seqs, causal=True, scale=SCALE, backward=False, device="cuda"):
         self.Tq, self.Tk, self.n_heads, self.n_seqs = Tq, Tk, n_heads, n_seqs
@@ -84,22 +90,22 @@ class LatentAttention:
 
     def _inputs(self, q, kv, k_rope, cu_q, cu_k):
         h = self.n_heads
-        B = cu_q.shape[0] - 1
-        if q.shape[0] != self.Tq or kv.shape[0] != self.Tk or k_rope.shape[0] != self.Tk:
-            raise ValueError(f"expected {self.Tq} queries and {self.Tk} keys")
+        B, Tq, Tk = cu_q.shape[0] - 1, q.shape[0], kv.shape[0]
+        if Tq > self.Tq or Tk > self.Tk or k_rope.shape[0] != Tk:
+            raise ValueError(f"at most {self.Tq} queries and {self.Tk} keys, as many rows of k_rope as of kv")
         if not 0 <= B <= self.n_seqs:
             raise ValueError(f"cu_q must describe at most {self.n_seqs} sequences")
         _vec(cu_q, "cu_q", torch.int32, (B + 1,))
         _vec(cu_k, "cu_k", torch.int32, (B + 1,))
         return (q, _rows(q, "q", (h, QK)), kv, _rows(kv, "kv", (h, NOPE + VALUE)), k_rope,
-                _rows(k_rope, "k_rope", (ROPE,))), B
+                _rows(k_rope, "k_rope", (ROPE,))), B, Tq, Tk
 
     def forward(self, q, kv, k_rope, cu_q, cu_k, stream=None):
-        """out [Tq, n_heads, 128] bf16 and lse [Tq, n_heads] fp32."""
-        ins, B = self._inputs(q, kv, k_rope, cu_q, cu_k)
-        L.moe_mla_attn_fwd(*ins, L.MOE_BF16, cu_q, cu_k, B, self.Tq, self.Tk, self.n_heads, self.causal,
-                           self.scale, self.out, self.n_heads * VALUE, self.lse, stream)
-        return self.out, self.lse
+        """out [q's rows, n_heads, 128] bf16 and lse [q's rows, n_heads] fp32."""
+        ins, B, Tq, Tk = self._inputs(q, kv, k_rope, cu_q, cu_k)
+        L.moe_mla_attn_fwd(*ins, L.MOE_BF16, cu_q, cu_k, B, Tq, Tk, self.n_heads, self.causal, self.scale, self.out,
+                           self.n_heads * VALUE, self.lse, stream)
+        return _first(self.out, Tq), _first(self.lse, Tq)
 
     __call__ = forward
 
@@ -108,13 +114,13 @@ class LatentAttention:
         if not self.has_backward:
             raise ValueError("built without backward=True")
         h = self.n_heads
-        ins, B = self._inputs(q, kv, k_rope, cu_q, cu_k)
-        if dout.shape[0] != self.Tq:
-            raise ValueError(f"expected {self.Tq} rows of dout")
+        ins, B, Tq, Tk = self._inputs(q, kv, k_rope, cu_q, cu_k)
+        if dout.shape[0] != Tq:
+            raise ValueError(f"expected {Tq} rows of dout")
         L.moe_mla_attn_bwd(dout, _rows(dout, "dout", (h, VALUE)), *ins, L.MOE_BF16, self.out, h * VALUE, self.lse,
-                           cu_q, cu_k, B, self.Tq, self.Tk, h, self.causal, self.scale, self.dq, h * QK, self.dkv,
+                           cu_q, cu_k, B, Tq, Tk, h, self.causal, self.scale, self.dq, h * QK, self.dkv,
                            h * (NOPE + VALUE), self.dk_rope, ROPE, self.ws, stream)
-        return self.dq, self.dkv, self.dk_rope
+        return _first(self.dq, Tq), _first(self.dkv, Tk), _first(self.dk_rope, Tk)
 
 
 class LatentExpand:

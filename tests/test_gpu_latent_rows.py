@@ -6,11 +6,10 @@ import numpy as np
 import pytest
 import torch
 
-import mixture_experts_layer_sigmoid_amd as moe
 from oracle import latent as ol
 from tests.gpu_util import log
 from tests.latent_util import decode_excess
-from tests.test_gpu_latent import DECODE, SCALE, Paged, _bf, _cu, _decode, _draw, _i32, _np
+from tests.test_gpu_latent import DECODE, SCALE, Paged, _cu, _decode, _draw, _i32, _np
 
 pytestmark = pytest.mark.gpu
 
