@@ -134,16 +134,22 @@ class LatentExpand:
         self.n_heads, self.max_tokens = w_kvb.shape[0], max_tokens
         self.w, _ = pack_weights(w_kvb.reshape(1, -1, LATENT).contiguous(), None, "bf16")
         self.out = torch.empty((max_tokens, self.n_heads, NOPE + VALUE), dtype=torch.bfloat16, device=w_kvb.device)
-        self.offsets = torch.tensor([0, max_tokens], dtype=torch.int32, device=w_kvb.device)
+        # the one expert's segment [0, T) of every T: a call of any size reads
+        # its row and writes nothing on the device
+        ends = torch.arange(max_tokens + 1, dtype=torch.int32)
+        self.offsets = torch.stack((torch.zeros_like(ends), ends), 1).to(w_kvb.device)
 
     def __call__(self, latents, stream=None):
-        """latents [max_tokens, 512] bf16, contiguous. Returns the object's
-        buffer [max_tokens, n_heads, 256]."""
-        _vec(latents, "latents", torch.bfloat16, (self.max_tokens, LATENT))
+        """latents [T, 512] bf16, contiguous, T at most max_tokens. Returns
+        [T, n_heads, 256], a view of the object's buffer."""
+        T = latents.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"at most {self.max_tokens} latents")
+        _vec(latents, "latents", torch.bfloat16, (T, LATENT))
         H = self.n_heads * (NOPE + VALUE)
-        L.moe_grouped_fc2(latents, None, L.MOE_BF16, self.w, None, L.MOE_BF16, self.offsets, 1, H, LATENT,
-                          self.max_tokens, self.out, L.MOE_BF16, stream)
-        return self.out
+        L.moe_grouped_fc2(latents, None, L.MOE_BF16, self.w, None, L.MOE_BF16, self.offsets[T], 1, H, LATENT, T,
+                          self.out, L.MOE_BF16, stream)
+        return _first(self.out, T)
 
 
 class LatentDecode:

@@ -1,10 +1,11 @@
 """The latent-attention classes with fewer rows than they are built for."""
+import numpy as np
 import pytest
 import torch
 
 import mixture_experts_layer_sigmoid_amd as moe
 from tests.gpu_util import log
-from tests.test_gpu_latent import _cu, _draw, _i32
+from tests.test_gpu_latent import _bf, _cu, _draw, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,20 @@ def test_attention_refuses_more_rows_and_uneven_ones(gpu_lib):
             a.forward(*bad, cu, cu)
     with pytest.raises(ValueError):
         a.backward(do[:4], q[:3], kv[:6], kr[:6], cu, cu)
+
+
+def test_expand_of_fewer_rows(gpu_lib):
+    """Every size up to the object's, bit for bit what an object of that size gives."""
+    log("latent expand of fewer rows")
+    g = np.random.default_rng(6)
+    c, w = _bf(g.standard_normal((140, 512))), _bf(g.standard_normal((2, 256, 512)) / 512 ** 0.5)
+    wide = moe.LatentExpand(w, max_tokens=140)
+    for n in (0, 1, 32, 77, 128, 129, 140):
+        wide.out.fill_(7.0)
+        got = wide(c[:n])
+        want = moe.LatentExpand(w, max_tokens=n)(c[:n])
+        torch.cuda.synchronize()
+        assert got.shape == (n, 2, 256) and torch.equal(got, want), n
+        assert (wide.out[n:] == 7).all(), n
+    with pytest.raises(ValueError):
+        moe.LatentExpand(w, max_tokens=139)(c)
