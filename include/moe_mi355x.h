@@ -666,7 +666,8 @@ int moe_bias_update(const int32_t* counts, int E, float gamma, const float* bias
  * bf16 as matrix operands.
  * *_ld: elements from one token's row to the next (a multiple of 8, at most
  * 2^23); a token's heads are consecutive. So a tensor may be a slice of wider
- * rows. scale: positive and finite.
+ * rows. scale: in (0, 2.3e38]; scaled scores have to stay within that too
+ * (both are multiplied by log2 e in fp32).
  * Packed sequences: cu [B + 1] int32 device, sequence b is rows [cu[b],
  * cu[b + 1]); values are clamped to the tensors, rows outside every sequence
  * are not written.

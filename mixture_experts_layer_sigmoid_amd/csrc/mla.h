@@ -33,6 +33,7 @@ constexpr int kR = 512;               // latent
 constexpr int kDc = kR + kDr;         // cache row
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMaxScale = 2.3e38f;  // its product with kLog2e is finite
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
@@ -259,7 +260,7 @@ inline int check_expanded(const std::string& fn, int fmt, int B, int Tq, int Tk,
               MOE_ERR_INVALID_ARG, fn + ": Tq * n_heads and Tk * n_heads must be <= 2^27, B * n_heads <= 2^22");
   MOE_REQUIRE(fmt == MOE_BF16, MOE_ERR_UNSUPPORTED, fn + ": fmt must be MOE_BF16");
   MOE_REQUIRE(causal == 0 || causal == 1, MOE_ERR_INVALID_ARG, fn + ": causal must be 0 or 1");
-  MOE_REQUIRE(scale > 0.f && scale <= 3.0e38f, MOE_ERR_INVALID_ARG, fn + ": scale must be positive and finite");
+  MOE_REQUIRE(scale > 0.f && scale <= kMaxScale, MOE_ERR_INVALID_ARG, fn + ": scale must be in (0, 2.3e38]");
   MOE_REQUIRE(q_ld >= static_cast<int64_t>(nh) * kDq && kv_ld >= static_cast<int64_t>(nh) * (kDn + kDv) &&
                   kr_ld >= kDr && out_ld >= static_cast<int64_t>(nh) * kDv && q_ld <= kMaxLd && kv_ld <= kMaxLd &&
                   kr_ld <= kMaxLd && out_ld <= kMaxLd,

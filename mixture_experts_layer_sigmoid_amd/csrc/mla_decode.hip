@@ -854,8 +854,8 @@ extern "C" int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, con
                   static_cast<int64_t>(page_size) * max_pages < (int64_t{1} << 31),
               MOE_ERR_INVALID_ARG,
               "moe_mla_decode: page_size, n_pages and max_pages must be >= 1, their products below 2^31");
-  MOE_REQUIRE(scale > 0.f && scale <= 3.0e38f, MOE_ERR_INVALID_ARG,
-              "moe_mla_decode: scale must be positive and finite");
+  MOE_REQUIRE(scale > 0.f && scale <= kMaxScale, MOE_ERR_INVALID_ARG,
+              "moe_mla_decode: scale must be in (0, 2.3e38]");
   MOE_REQUIRE(q_ld >= static_cast<int64_t>(n_heads) * kDq && out_ld >= static_cast<int64_t>(n_heads) * kDv &&
                   q_ld <= kMaxLd && out_ld <= kMaxLd,
               MOE_ERR_INVALID_ARG, "moe_mla_decode: a row stride is smaller than its row or above 2^23 elements");
