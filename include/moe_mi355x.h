@@ -707,6 +707,11 @@ size_t moe_mla_attn_bwd_workspace(int Tq, int Tk, int n_heads);
  *   over the heads in fp32), bf16 out; keys that no query sees get 0.
  * Other arguments and limits as moe_mla_attn_fwd. The results do not depend
  * on the order in which workgroups run (no atomics).
+ * Every row of q, kv, k_rope, out and dout that a sequence holds must be
+ * finite, also where the mask hides it and where a query has no keys (lse
+ * -inf): its weight 0 still multiplies it, as in the formula's matrix
+ * products, and which other rows that reaches is not defined. Rows outside
+ * every sequence may hold anything.
  */
 int moe_mla_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q_ld,
                      const void* kv, int64_t kv_ld, const void* k_rope, int64_t kr_ld,
@@ -729,8 +734,9 @@ int moe_mla_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q
  * cos, sin both NULL: no rotation (positions is then not read). Positions
  *          outside [0, max_pos) take the nearest row.
  * slots    [T] int64: cache row (page * page_size + place) of each token;
- *          values outside [0, n_slots) write nothing (padding tokens). Two
- *          tokens with one slot leave either's row.
+ *          values outside [0, n_slots) write nothing (padding tokens). Where
+ *          two tokens have one slot, its row holds pieces of either, in no
+ *          defined mix (the other rows are not touched).
  * cache    [n_slots, 576] bf16.
  * q, q_out [T, n_heads, 192], both NULL or both given; q_out may equal q
  *          (with qo_ld == q_ld) and must not overlap it otherwise.
