@@ -17,20 +17,26 @@
 // p and ds are rounded to bf16 as operands of dv, dk and dq (the matrix
 // instruction's type; rms 2^-9.2 of each element, so a gradient, a sum of
 // many, keeps that relative error: 2.5e-3 rms against 64 bits with its own
-// rounding at the store); scores, dp, delta and all sums are fp32.
+// rounding at the store). delta is formed from the stored out, which is
+// rounded to bf16 and a sum of rounded weights (keeping it in fp32 would be
+// another output of the forward, twice out's bytes); scores, dp, delta's sum
+// and all other sums are fp32.
 //
 // Bound by the products and their operands from LDS: seven products of pairs
 // x 128..192 (the formulas' five, scores and dp once more) = 1.44 TFLOP with
-// the diagonal's tiles at 4096 tokens x 128 heads, causal; the gradients' kernel takes 1632-1668 us =
-// 860-880 TFLOP/s (matrix unit 43% busy; an 8192^3 bf16 product reaches 1369).
-// The kept side's operands and sums fill the 512 registers of a wave (kv: 80
-// operand, 160 sum, 64 score registers), so there is one wave a SIMD, and what
-// overlaps is written out: operands are read kAhead products ahead, and one
-// block's element-wise work runs between another's products. A tile of 64
+// the diagonal's tiles at 4096 tokens x 128 heads, causal; the gradients'
+// kernel takes 1650 us on average of 20 calls (1514 for the first to 2038: the
+// clock falls under this load) = 870 TFLOP/s (matrix unit 43% busy; an 8192^3
+// bf16 product reaches 1369). The kept side's operands and sums (kv: 80
+// operand, 160 sum, 64 score registers) bring a wave to 194 + 224 of 512
+// registers, too many for two waves a SIMD; 81 of 160 KB LDS. What overlaps is
+// written out: operands are read kAhead products ahead, and one block's
+// element-wise work runs between another's products. A tile of 64
 // queries takes 4.7k cycles against 2560 of products, a tile of 64 keys in the
 // other part 3.4k against 2048; start and end (operands in, sums out through
-// LDS) about 20k a workgroup. Statistics (47 us) and rotary sums (27 us) run at
-// the rate of a copy. 515 tokens x 16 heads: 3.3 + 24.4 + 4.4 us, latency.
+// LDS) about 20k a workgroup, 15 to 25% of an average one here. Statistics (47
+// us) and rotary sums (27 us) run at the rate of a copy. 515 tokens x 16 heads:
+// 3.5 + 24.3 + 4.5 us: a workgroup walks up to seven tiles one after another.
 // Measured and slower: nothing read ahead and two waves a SIMD for dq (1169 +
 // 901 us for the two parts, against 954 + 779 then), two launches for the parts
 // (1733), three stages with the barrier in mid-tile (1693), three blocks in

@@ -19,11 +19,12 @@
 // of issue), which two waves a SIMD overlap. Four waves (128 queries) a
 // workgroup and two workgroups a CU: keys and values pass LDS in tiles of 64,
 // double buffered (80 KB a workgroup), loaded without registers. 3048 queries
-// behind 11169 more keys x 128 heads 1740-1850 us = 940-1000 TFLOP/s (matrix
+// behind 11169 more keys x 128 heads 1835 us on average of 20 calls = 950
+// TFLOP/s (1720 for the first to 2190: the clock falls under this load; matrix
 // unit 57% busy; an 8192^3 bf16 product reaches 1369); 4096 tokens of three
-// prompts, causal, 374-445 us = 660-790, where the short rows of the mask's
+// prompts, causal, 443 us (375-502) = 665, where the short rows of the mask's
 // diagonal tiles and each workgroup's start (queries, first tile) count; 168
-// tokens x 16 heads 8.7 us. Measured and slower: eight waves a workgroup (489
+// tokens x 16 heads 8.8 us. Measured and slower: eight waves a workgroup (489
 // against 440 us), 64 queries a wave at one wave a SIMD (560; 1951 against
 // 1800 us: the softmax no longer runs under another wave's products).
 #include "mla.h"

@@ -15,20 +15,34 @@
 // Roundings: q_lat to bf16 and the weights p to bf16 (both operands of matrix
 // instructions, rms 2^-9.2 of each; a wider q_lat would double the products
 // of the scores); o_lat stays fp32 up to W_UV, where it enters as two bf16
-// terms. Scores, references, sums and pieces are fp32. Against 64 bits out has
-// 1.8e-3 to 2.5e-3 rms, 1.66e-3 of it the output's own rounding; q_lat's shows
-// most where a row has few keys.
+// terms. A weight is rounded once more where the two halves of a token tile
+// have other references and its own is brought to the larger. References in
+// whole powers of two would spare that, but then the largest key's weight is
+// no longer exactly 1, which costs more: out 2.60e-3 rms instead of 1.73e-3 (8
+// long caches with lone tokens among them), 2.38 instead of 1.92 (64 ragged
+// requests), 2.51 instead of 2.15 (trees of 32), the time the same. Scores,
+// references, sums and pieces are fp32. Against 64 bits out has 1.7e-3 to
+// 2.6e-3 rms: at 531 cached tokens 2.55e-3, the root of the squares of the
+// output's own rounding (1.67), q_lat's (1.44) and the weights' (1.30).
 //
 // Bound, by size (an 8192^3 bf16 product reaches 1369 TFLOP/s here, a copy
 // 4.87 TB/s):
-//   256 tokens of 8 trees x 128 heads: 291 us attention = 740 TFLOP/s, operands
-//     through LDS (a value operand serves two row blocks; matrix unit 39% busy);
-//   64 ragged requests x 128 heads: 82 us, of it the pieces' starts and ends
-//     (queries in, sums out: about 18k cycles a piece against 4.9k a tile of 64
-//     tokens and 64 rows); join 20, q_lat 7.6 us;
+//   256 tokens of 8 trees x 128 heads: 294 us attention (274-312) = 730
+//     TFLOP/s. A tile of 64 tokens and 64 rows takes 4.9k cycles for 2.2k of
+//     products: scores, softmax and value products follow one another between
+//     barriers at one wave a SIMD (matrix unit 39% busy); join 42, q_lat 17;
+//   64 ragged requests x 128 heads: 83-85 us, the same tiles (a workgroup has 22
+//     on average, four fifths of its time) and the pieces' starts and ends
+//     (queries in, sums out: about 18k cycles a piece, 1.4 a workgroup); matrix
+//     unit 29% busy; join 20, q_lat 7.5 us;
 //   8 long caches x 16 heads, 279k cached tokens: 63 us = 5.1 TB/s, at the
 //     rate of a copy; join 14.5 us (its pieces' traffic);
-//   one request x 16 heads, 531 tokens: 2.9 + 10.0 + 6.7 us, latency.
+//   one request x 16 heads, 531 tokens: 3 + 10 + 6.7 us, latency.
+// The attention fills its registers: 256 and 230 to 250 accumulation registers
+// a wave, one wave a SIMD; 61 to 69 scalar values (the work list's, page
+// addresses) live in vector lanes. With 32 rows a workgroup has two waves and
+// 148 KB of LDS, so two of a compute unit's four SIMDs are empty; long caches
+// run at a copy's rate all the same.
 #include "mla.h"
 
 #include <cmath>
@@ -496,7 +510,8 @@ void decode_attn_kernel(DecodeArgs p) {
       if (tail && (p.tree || sq.nq > 1)) {
         // a hidden token's row is still in the value product, with weight 0:
         // values that are not finite must not reach it (rows that see the
-        // token have them in their scores already)
+        // token have them in their scores already, as NaN, or with the whole
+        // weight, or as -inf, which takes no weight)
         for (int i = threadIdx.x; i < kLat / 16; i += 64 * NW) {
           u32x4_t v = *reinterpret_cast<const u32x4_t*>(buf + i * 16);
           if (drop_nonfinite(v)) *reinterpret_cast<u32x4_t*>(buf + i * 16) = v;
@@ -605,9 +620,12 @@ void decode_attn_kernel(DecodeArgs p) {
 // A workgroup takes one head of `toks` tokens (up to 32; fewer when there are
 // few, so that the pieces' rows are read by enough workgroups). A wave joins
 // the pieces of TPW tokens side by side (below 4 tokens several waves share
-// one token's pieces), and puts the rows into LDS as two bf16 terms (16
+// one token's pieces in turn and their sums are added after), in an order that
+// depends on the sizes alone, and puts the rows into LDS as two bf16 terms (16
 // significant bits, so the product adds no rounding of its own); then each
-// wave computes 32 of the 128 value columns.
+// wave computes 32 of the 128 value columns. Pieces, conversion, barrier, W_UV
+// and products follow one another: 42 us for 84 MB = 2 TB/s (256 tokens x 128
+// heads). With TPW 8, 56 scalar values live in vector lanes (6 with TPW 4).
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
