@@ -792,6 +792,174 @@ int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, const void* w_
                    int n_heads, float scale, void* out, int64_t out_ld, float* lse,
                    void* ws, size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Grouped-query attention — the attention of layers whose experts stand behind
+ * n_heads query heads that share n_kv_heads key and value heads (n_heads a
+ * multiple of n_kv_heads, up to 1024; query head h takes key head h / G, G =
+ * n_heads / n_kv_heads). Heads have head_dim = 64 or 128 values; tensors are
+ * bf16 (fmt = MOE_BF16; anything else is MOE_ERR_UNSUPPORTED). *_ld, scale and
+ * packed sequences as for latent attention above; sums, softmax statistics
+ * and lse are fp32, weights and score gradients are rounded to bf16 as matrix
+ * operands.
+ */
+
+/*
+ * moe_qk_norm_rope — RMS norm of every head's query and key with the rotation
+ * of their first `rotary` values, in one pass, per token t and head:
+ *   u = x / sqrt(mean(x^2) + eps) * w,  w = w_q for queries, w_k for keys
+ *   out = u with pair i < rotary / 2 turned by the angle of row positions[t]:
+ *   (a cos - b sin, a sin + b cos)
+ * Pair i is values (2 i, 2 i + 1) with interleaved = 1, (i, i + rotary / 2)
+ * with 0; values from `rotary` on are not turned. fp32 arithmetic, one rounding.
+ * q [T, n_heads, head_dim] and q_out, k [T, n_kv_heads, head_dim] and k_out:
+ *          rows q_ld, qo_ld, k_ld, ko_ld apart (slices of one projection's
+ *          rows). An output may be its input (same stride) and must not
+ *          overlap any tensor otherwise. n_heads and n_kv_heads in [1, 1024]
+ *          need not be multiples here.
+ * w_q, w_k [head_dim] bf16, either may be NULL: those heads are not
+ *          normalized.
+ * cos, sin [max_pos, rotary / 2] fp32, both NULL: no rotation (positions and
+ *          rotary are then not used). rotary: a multiple of 16 up to head_dim.
+ *          Positions [T] int32 outside [0, max_pos) take the nearest row.
+ * Limits: T <= 2^23, eps in [0, 1]. T == 0 is a no-op.
+ */
+int moe_qk_norm_rope(const void* q, int64_t q_ld, const void* k, int64_t k_ld, int fmt,
+                     const void* w_q, const void* w_k, float eps, const float* cos,
+                     const float* sin, int max_pos, const int32_t* positions, int rotary,
+                     int interleaved, int T, int n_heads, int n_kv_heads, int head_dim,
+                     void* q_out, int64_t qo_ld, void* k_out, int64_t ko_ld,
+                     hipStream_t stream);
+
+/* moe_qk_norm_rope_bwd_workspace — bytes of moe_qk_norm_rope_bwd's workspace
+ * (0 for a bad head_dim). */
+size_t moe_qk_norm_rope_bwd_workspace(int head_dim);
+
+/*
+ * moe_qk_norm_rope_bwd — gradients of moe_qk_norm_rope from the gradients
+ * dq_out, dk_out of its outputs and its inputs: dq, dk (bf16, shapes of q, k)
+ * and dw_q, dw_k [head_dim] fp32, summed over tokens and heads in an order that
+ * depends on T alone. A side without weight has no dw (may be NULL, is not
+ * written), and its x is not read (may be NULL). Outputs must not overlap any
+ * tensor. ws: needed where either weight is given. With T == 0 the weights'
+ * gradients are zero. Other arguments and limits as moe_qk_norm_rope.
+ */
+int moe_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ld, const void* dk_out,
+                         int64_t dko_ld, const void* q, int64_t q_ld, const void* k,
+                         int64_t k_ld, int fmt, const void* w_q, const void* w_k, float eps,
+                         const float* cos, const float* sin, int max_pos,
+                         const int32_t* positions, int rotary, int interleaved, int T,
+                         int n_heads, int n_kv_heads, int head_dim, void* dq, int64_t dq_ld,
+                         void* dk, int64_t dk_ld, float* dw_q, float* dw_k, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
+
+/*
+ * moe_gqa_attn_fwd — attention over packed sequences (prompts, training):
+ *   s[i, j] = scale * q[i, h] . k[j, h / G]
+ *   out[i, h] = sum_j softmax_j(s[i, :]) v[j, h / G],  lse[i, h] = log sum_j exp s[i, j]
+ * q [Tq, n_heads, head_dim], k and v [Tk, n_kv_heads, head_dim], out as q,
+ * lse [Tq, n_heads] fp32 (optional).
+ * causal   1: query i of a sequence with n_q queries and n_k keys sees keys
+ *          j <= i + n_k - n_q (the last query sees every key); 0: all keys.
+ * A query without keys gives out 0 and lse -inf. A key that is hidden from
+ * some queries of its sequence and shown to others must have a finite value
+ * row: its weight 0 still multiplies it, as in the formula's matrix product.
+ * Limits: Tq * n_heads and Tk * n_heads <= 2^27, B * n_heads <= 2^22. Tq == 0
+ * or B == 0 is a no-op.
+ */
+int moe_gqa_attn_fwd(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v,
+                     int64_t v_ld, int fmt, const int32_t* cu_q, const int32_t* cu_k, int B,
+                     int Tq, int Tk, int n_heads, int n_kv_heads, int head_dim, int causal,
+                     float scale, void* out, int64_t out_ld, float* lse, hipStream_t stream);
+
+/* moe_gqa_attn_bwd_workspace — bytes of moe_gqa_attn_bwd's workspace; it does
+ * not shrink as Tq or Tk grow, so one for the largest call serves all (0 for
+ * bad sizes). */
+size_t moe_gqa_attn_bwd_workspace(int Tq, int Tk, int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * moe_gqa_attn_bwd — gradients of moe_gqa_attn_fwd, from the gradient dout of
+ * out and the forward's inputs, out and lse: dq (as q), dk and dv (as k, v;
+ * summed in fp32 over the queries of all heads of the group), bf16 out; keys
+ * that no query sees get 0. Other arguments and limits as moe_gqa_attn_fwd.
+ * The results do not depend on the order in which workgroups run (no atomics).
+ * Every row of q, k, v, out and dout that a sequence holds must be finite,
+ * also where the mask hides it: its weight 0 still multiplies it. Rows outside
+ * every sequence may hold anything.
+ */
+int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q_ld,
+                     const void* k, int64_t k_ld, const void* v, int64_t v_ld, int fmt,
+                     const void* out, int64_t out_ld, const float* lse, const int32_t* cu_q,
+                     const int32_t* cu_k, int B, int Tq, int Tk, int n_heads, int n_kv_heads,
+                     int head_dim, int causal, float scale, void* dq, int64_t dq_ld, void* dk,
+                     int64_t dk_ld, void* dv, int64_t dv_ld, void* ws, size_t ws_bytes,
+                     hipStream_t stream);
+
+/*
+ * The 8-bit paged cache: E4M3 codes, for every 16 tokens of a key head one
+ * power-of-two scale for the keys and one for the values (a byte e + 127;
+ * value = code * 2^e). Page p, head h, block b of 16 tokens, its token t:
+ *   keys    k_cache[p, h, b, d / 16, t, d % 16]
+ *   values  v_cache[p, h, b, d / 2, (t / 4) % 2, d % 2, t / 8, t % 4]
+ *   scales  k_scales[p, h, b], v_scales[p, h, b]
+ * page_size: a multiple of 16. page_table [B, max_pages] int32: request b's
+ * token j is in page page_table[b, j / page_size] (ids outside [0, n_pages)
+ * take the nearest page). lens [B] int32: tokens of request b in the cache,
+ * the call's n new ones (rows [cu[b], cu[b + 1]) of its tensors) included as
+ * the last; clamped to max_pages * page_size. With fewer tokens than rows the
+ * first rows have no place: they are not stored, and see nothing.
+ * Limits: B <= 65536, B * n_kv_heads <= 2^19, T * n_kv_heads <= 2^24 (decode:
+ * T * n_heads), the cache's blocks (n_pages * n_kv_heads * page_size / 16) < 2^31, page_size *
+ * max_pages <= 2^30. B == 0 or T == 0 is a no-op.
+ */
+
+/*
+ * moe_gqa_append — new keys and values into the cache. A block's scale is the
+ * smallest that brings the largest magnitude of the tokens it holds within
+ * 448, codes are rounded to nearest even; when new tokens raise the scale, the
+ * codes of the block's earlier tokens (positions before the request's new
+ * ones) are rounded again under it (they keep their digits down to the codes'
+ * smallest normal number, 2^-6 of the scale). Bytes of later positions are not
+ * changed. So a token gives the same codes in whichever pieces its request
+ * arrives, up to that second rounding. Two requests of a call must not write
+ * to the same block.
+ * k, v     [T, n_kv_heads, head_dim] bf16, rows k_ld, v_ld apart. Values are
+ *          expected to be finite and below 2^127: NaN and infinities become
+ *          NaN codes, and an infinity brings its block to the largest scale.
+ */
+int moe_gqa_append(const void* k, int64_t k_ld, const void* v, int64_t v_ld, int fmt,
+                   void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales,
+                   int page_size, int n_pages, const int32_t* page_table, int max_pages,
+                   const int32_t* lens, const int32_t* cu, int B, int T, int n_kv_heads,
+                   int head_dim, hipStream_t stream);
+
+/* moe_gqa_decode_workspace — bytes of moe_gqa_decode's workspace for up to T
+ * new tokens of up to B requests (it grows with both; 0 for bad sizes). */
+size_t moe_gqa_decode_workspace(int B, int T, int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * moe_gqa_decode — attention of the last tokens of B requests over the cache
+ * (serving: single tokens, drafted tokens, trees of drafted tokens):
+ *   s[j] = scale * q[t, h] . k_j,  out[t, h] = sum_j softmax_j(s) v_j,
+ *   lse[t, h] = log sum_j exp s[j]
+ * q [T, n_heads, head_dim] rows q_ld apart, out as q, lse [T, n_heads] fp32
+ * (optional). A request's new tokens are in the cache already.
+ * tree_mask NULL: new token i sees the earlier tokens and new tokens <= i.
+ *          [T] int64: new token i sees the earlier tokens and, of its
+ *          request's new tokens, those whose bit is set in tree_mask (bit j:
+ *          new token j; up to 64 new tokens a request, later ones are
+ *          hidden). Set the token's own bit to let it see itself.
+ * What the cache holds behind a request's length is never used, and NaN codes
+ * of tokens that a new token does not see do not reach it. A token that sees
+ * nothing gives out 0 and lse -inf.
+ * ws       moe_gqa_decode_workspace(B, T, ...) bytes.
+ */
+int moe_gqa_decode(const void* q, int64_t q_ld, int fmt, const void* k_cache,
+                   const void* v_cache, const uint8_t* k_scales, const uint8_t* v_scales,
+                   int page_size, int n_pages, const int32_t* page_table, int max_pages,
+                   const int32_t* lens, const int32_t* cu_q, const int64_t* tree_mask, int B,
+                   int T, int n_heads, int n_kv_heads, int head_dim, float scale, void* out,
+                   int64_t out_ld, float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,9 @@ and NVFP4 quantization) runs in the hand-written HIP library libmoe_mi355x.so be
 the C ABI of include/moe_mi355x.h. This package is its Python binding: the
 functions in `_lib` carry the C names and only marshal arguments; `layer`
 strings them into a forward pass, `mla` holds the latent attention beside it
-(expanded form with its backward, absorbed form over a paged cache). There is no CPU fallback: every binding call
+(expanded form with its backward, absorbed form over a paged cache), `gqa`
+grouped-query attention (norms with rotation, packed sequences with their
+backward, an 8-bit paged cache). There is no CPU fallback: every binding call
 loads the built library and raises when it is missing.
 """
 from ._lib import (  # noqa: F401
@@ -23,8 +25,11 @@ from ._lib import (  # noqa: F401
     moe_grouped_fc2_nvfp4,
     moe_mla_attn_fwd, moe_mla_attn_bwd, moe_mla_attn_bwd_workspace, moe_mla_append, moe_mla_decode,
     moe_mla_decode_workspace,
+    moe_qk_norm_rope, moe_qk_norm_rope_bwd, moe_qk_norm_rope_bwd_workspace, moe_gqa_attn_fwd, moe_gqa_attn_bwd,
+    moe_gqa_attn_bwd_workspace, moe_gqa_append, moe_gqa_decode, moe_gqa_decode_workspace,
     SIGNATURES, LIB_PATH,
 )
 from .layer import (MoEForward, MoEBackward, RouterBackward, ExpertWeights, bias_update,  # noqa: F401
                     quantize_mx, quantize_mx_t, FMT)
 from .mla import LatentAttention, LatentDecode, LatentExpand, latent_cache_append  # noqa: F401
+from .gqa import GroupedAttention, GroupedCache, GroupedDecode, QKNormRope, grouped_cache_append  # noqa: F401

@@ -67,6 +67,21 @@ SIGNATURES = {
     "moe_mla_decode_workspace": (_SZ, [_I, _I]),
     "moe_mla_decode": (_I, [_P, _I64, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _I, _I, _I, _F, _P,
                             _I64, _P, _P, _SZ, _P]),
+    "moe_qk_norm_rope": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _F, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                              _P, _I64, _P, _I64, _P]),
+    "moe_qk_norm_rope_bwd_workspace": (_SZ, [_I]),
+    "moe_qk_norm_rope_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _F, _P, _P, _I, _P,
+                                  _I, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]),
+    "moe_gqa_attn_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P,
+                              _I64, _P, _P]),
+    "moe_gqa_attn_bwd_workspace": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_gqa_attn_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _P, _I64, _P, _P, _P, _I, _I, _I,
+                              _I, _I, _I, _I, _F, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "moe_gqa_append": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I,
+                            _P]),
+    "moe_gqa_decode_workspace": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_gqa_decode": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I,
+                            _F, _P, _I64, _P, _P, _SZ, _P]),
     "moe_grouped_mlp_bwd_workspace": (_SZ, [_I, _I, _I, _I, _I, _I64, _I]),
     "moe_grouped_mlp_bwd": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                  _I, _I64, _P, _P, _P, _P, _SZ, _P]),
@@ -369,3 +384,69 @@ def moe_mla_decode(q, q_ld, w_uk, w_uv, fmt, cache, page_size, n_pages, page_tab
         _ptr(q), q_ld, _ptr(w_uk), _ptr(w_uv), fmt, _ptr(cache), page_size, n_pages, _ptr(page_table),
         max_pages, _ptr(lens), _ptr(cu_q), _ptr(tree_mask), B, T, n_heads, scale, _ptr(out), out_ld,
         _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_qk_norm_rope(q, q_ld, k, k_ld, fmt, w_q, w_k, eps, cos, sin, max_pos, positions, rotary,
+                     interleaved, T, n_heads, n_kv_heads, head_dim, q_out, qo_ld, k_out, ko_ld,
+                     stream=None):
+    _check("moe_qk_norm_rope", load().moe_qk_norm_rope(
+        _ptr(q), q_ld, _ptr(k), k_ld, fmt, _ptr(w_q), _ptr(w_k), eps, _ptr(cos), _ptr(sin), max_pos,
+        _ptr(positions), rotary, interleaved, T, n_heads, n_kv_heads, head_dim, _ptr(q_out), qo_ld,
+        _ptr(k_out), ko_ld, _stream(stream)))
+
+
+def moe_qk_norm_rope_bwd_workspace(head_dim) -> int:
+    return load().moe_qk_norm_rope_bwd_workspace(head_dim)
+
+
+def moe_qk_norm_rope_bwd(dq_out, dqo_ld, dk_out, dko_ld, q, q_ld, k, k_ld, fmt, w_q, w_k, eps, cos, sin,
+                         max_pos, positions, rotary, interleaved, T, n_heads, n_kv_heads, head_dim, dq,
+                         dq_ld, dk, dk_ld, dw_q, dw_k, ws, stream=None):
+    _check("moe_qk_norm_rope_bwd", load().moe_qk_norm_rope_bwd(
+        _ptr(dq_out), dqo_ld, _ptr(dk_out), dko_ld, _ptr(q), q_ld, _ptr(k), k_ld, fmt, _ptr(w_q),
+        _ptr(w_k), eps, _ptr(cos), _ptr(sin), max_pos, _ptr(positions), rotary, interleaved, T, n_heads,
+        n_kv_heads, head_dim, _ptr(dq), dq_ld, _ptr(dk), dk_ld, _ptr(dw_q), _ptr(dw_k), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_gqa_attn_fwd(q, q_ld, k, k_ld, v, v_ld, fmt, cu_q, cu_k, B, Tq, Tk, n_heads, n_kv_heads,
+                     head_dim, causal, scale, out, out_ld, lse, stream=None):
+    _check("moe_gqa_attn_fwd", load().moe_gqa_attn_fwd(
+        _ptr(q), q_ld, _ptr(k), k_ld, _ptr(v), v_ld, fmt, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, n_heads,
+        n_kv_heads, head_dim, causal, scale, _ptr(out), out_ld, _ptr(lse), _stream(stream)))
+
+
+def moe_gqa_attn_bwd_workspace(Tq, Tk, n_heads, n_kv_heads, head_dim) -> int:
+    return load().moe_gqa_attn_bwd_workspace(Tq, Tk, n_heads, n_kv_heads, head_dim)
+
+
+def moe_gqa_attn_bwd(dout, dout_ld, q, q_ld, k, k_ld, v, v_ld, fmt, out, out_ld, lse, cu_q, cu_k, B, Tq,
+                     Tk, n_heads, n_kv_heads, head_dim, causal, scale, dq, dq_ld, dk, dk_ld, dv, dv_ld,
+                     ws, stream=None):
+    _check("moe_gqa_attn_bwd", load().moe_gqa_attn_bwd(
+        _ptr(dout), dout_ld, _ptr(q), q_ld, _ptr(k), k_ld, _ptr(v), v_ld, fmt, _ptr(out), out_ld,
+        _ptr(lse), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, n_heads, n_kv_heads, head_dim, causal, scale,
+        _ptr(dq), dq_ld, _ptr(dk), dk_ld, _ptr(dv), dv_ld, _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_gqa_append(k, k_ld, v, v_ld, fmt, k_cache, v_cache, k_scales, v_scales, page_size, n_pages,
+                   page_table, max_pages, lens, cu, B, T, n_kv_heads, head_dim, stream=None):
+    _check("moe_gqa_append", load().moe_gqa_append(
+        _ptr(k), k_ld, _ptr(v), v_ld, fmt, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        page_size, n_pages, _ptr(page_table), max_pages, _ptr(lens), _ptr(cu), B, T, n_kv_heads, head_dim,
+        _stream(stream)))
+
+
+def moe_gqa_decode_workspace(B, T, n_heads, n_kv_heads, head_dim) -> int:
+    return load().moe_gqa_decode_workspace(B, T, n_heads, n_kv_heads, head_dim)
+
+
+def moe_gqa_decode(q, q_ld, fmt, k_cache, v_cache, k_scales, v_scales, page_size, n_pages, page_table,
+                   max_pages, lens, cu_q, tree_mask, B, T, n_heads, n_kv_heads, head_dim, scale, out,
+                   out_ld, lse, ws, stream=None):
+    _check("moe_gqa_decode", load().moe_gqa_decode(
+        _ptr(q), q_ld, fmt, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), page_size,
+        n_pages, _ptr(page_table), max_pages, _ptr(lens), _ptr(cu_q), _ptr(tree_mask), B, T, n_heads,
+        n_kv_heads, head_dim, scale, _ptr(out), out_ld, _ptr(lse), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))

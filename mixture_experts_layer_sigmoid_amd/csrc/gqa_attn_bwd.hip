@@ -1,0 +1,602 @@
+// moe_gqa_attn_bwd: gradients of moe_gqa_attn_fwd.
+//
+// With p the softmax weights, do the output's gradient:
+//   delta[i] = do[i] . out[i]          (= sum_j p[i, j] dp[i, j])
+//   dp = do v^T,  ds = p (dp - delta),  dv = p^T do
+//   dq = scale ds k,  dk = scale ds^T q,  dk and dv summed over the queries of
+//   all heads of the group
+// p is computed again from the scores and the forward's lse.
+//
+// The row statistics (lse in base 2, delta) come first, then the gradients:
+// one kind of workgroup keeps 32 keys a wave and walks the packed rows (dk, dv:
+// the heads of the group are rows among others, so their sum needs no further
+// step), the other keeps 32 packed rows a wave and walks the keys (dq). The
+// scores are computed twice, so nothing is added up by atomics and the result
+// does not depend on the order in which workgroups run. With few keys the rows
+// are cut into parts whose dk and dv (fp32) a last launch adds up in order.
+//
+// p and ds are rounded to bf16 as operands of dv, dk and dq (the matrix
+// instruction's type; rms 2^-9.2 of each element). delta is formed from the
+// stored out, which is rounded to bf16; scores, dp, delta's sum and all other
+// sums are fp32.
+#include "gqa.h"
+
+#include <cmath>
+
+namespace moe {
+namespace gqa {
+namespace {
+
+struct BwdArgs {
+  const uint16_t* dout;
+  int64_t dout_ld;
+  const uint16_t* q;
+  int64_t q_ld;
+  const uint16_t* k;
+  int64_t k_ld;
+  const uint16_t* v;
+  int64_t v_ld;
+  const uint16_t* out;
+  int64_t out_ld;
+  const float* lse;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int B, Tq, Tk, nh, nkv, causal;
+  Div g;
+  float scale;
+  uint16_t* dq;
+  int64_t dq_ld;
+  uint16_t* dk;
+  int64_t dk_ld;
+  uint16_t* dv;
+  int64_t dv_ld;
+  float2* stats;          // [Tq, nh]: (lse in base 2, delta); a row without keys: (+inf, 0)
+  float* part;            // [parts, Tk, nkv, 2, D]: dk (not scaled) and dv of each part
+  int parts;
+  int k_tiles, q_tiles;   // workgroups per key head (and part) of the two kinds
+};
+
+// D / 8 lanes per (token, head) row
+template <int D>
+__global__ __launch_bounds__(256) void bwd_stats_kernel(BwdArgs p) {
+  constexpr int kL = D / 8;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / kL) + threadIdx.x / kL;
+  if (row >= static_cast<int64_t>(p.Tq) * p.nh) return;
+  const int64_t t = row / p.nh;
+  const int h = static_cast<int>(row - t * p.nh);
+  const int c = (threadIdx.x & (kL - 1)) * 8;
+  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p.out + t * p.out_ld + h * D + c);
+  const u32x4_t b = *reinterpret_cast<const u32x4_t*>(p.dout + t * p.dout_ld + h * D + c);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
+    s = fmaf(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u), s);
+  }
+#pragma unroll
+  for (int o = kL / 2; o >= 1; o >>= 1) s += __shfl_xor(s, o, kL);
+  if ((threadIdx.x & (kL - 1)) == 0) {
+    const float l = p.lse[row];
+    const bool none = l == -INFINITY;
+    p.stats[row] = none ? make_float2(INFINITY, 0.f) : make_float2(l * kLog2e, s);
+  }
+}
+
+// LDS offsets of the operands of one stage: a tile of RB-byte rows, and a
+// second one behind it that is read with the first's offsets. They move with
+// the stage in use, so no address is computed between the products.
+template <int RB>
+struct Operands {
+  uint32_t row[RB / 32], col[RB / 64][2];
+  __device__ __forceinline__ explicit Operands(int lane) {
+#pragma unroll
+    for (int s = 0; s < RB / 32; ++s) row[s] = row_operand_offset<RB>(lane, s);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < RB / 64; ++c) col[c][h] = col_operand_offset<RB>(lane, c, h);
+  }
+  __device__ __forceinline__ void move(int by) {
+#pragma unroll
+    for (int s = 0; s < RB / 32; ++s) row[s] += by;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < RB / 64; ++c) col[c][h] += by;
+  }
+};
+
+constexpr int kWaves = 4;
+constexpr int kTile = 64;                               // rows or keys that pass by at a time
+constexpr int kSide = 32 * kWaves;                      // keys or rows that a workgroup keeps
+constexpr int kAhead = 5;                               // matrix operands read ahead
+template <int D>
+constexpr int stage_bytes() { return 2 * kTile * D * 2 + kTile * 8; }
+
+// ---- dk, dv: a wave keeps 32 keys (the lanes' columns), packed rows pass by ----
+template <int D>
+__device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int tile_index, uint8_t* smem) {
+  constexpr int RB = D * 2, S = D / 16, C = D / 32;
+  constexpr int kDo = kTile * RB;                       // dO's place behind Q's
+  constexpr int kStat = 2 * kTile * RB, kStage = stage_bytes<D>();
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const SeqTile st = find_rows(p.cu_k, p.cu_q, p.B, p.Tk, p.Tq, 1, kSide, tile_index);
+  if (st.b < 0) return;
+  const int n_k = st.n;
+  const int q_start = st.start2, n_q = st.n2, n_rows = n_q * p.g.d;
+  const int k0 = st.tile * kSide;
+  const int key = k0 + wave * 32 + (lane & 31);
+  const int keyc = key < n_k ? key : n_k - 1;
+  const int shift = p.causal ? n_k - n_q : n_k;                // query i sees keys <= i + shift
+  auto first_row = [&](int j) { return clamp_int(j - shift, 0, n_q) * p.g.d; };   // that sees key j
+  const int t_lo = first_row(k0) / kTile, t_hi = (n_rows + kTile - 1) / kTile;
+  const int n_t = t_hi > t_lo ? t_hi - t_lo : 0;
+  const int t_first = t_lo + static_cast<int>(static_cast<int64_t>(n_t) * part / p.parts);
+  const int t_end = t_lo + static_cast<int>(static_cast<int64_t>(n_t) * (part + 1) / p.parts);
+  const int row_min = first_row(keyc);                         // rows before it do not see this lane's key
+
+  const uint16_t* q = p.q + static_cast<int64_t>(q_start) * p.q_ld + head * p.g.d * D;
+  const uint16_t* dout = p.dout + static_cast<int64_t>(q_start) * p.dout_ld + head * p.g.d * D;
+  const float2* stats = p.stats + static_cast<int64_t>(q_start) * p.nh + head * p.g.d;
+  float2 stat_next = make_float2(INFINITY, 0.f);
+  auto load = [&](int t, uint8_t* buf) {
+    rows_load<RB, kTile, kWaves>(q, p.q_ld, p.g, t * kTile, n_rows, buf, wave, lane);
+    rows_load<RB, kTile, kWaves>(dout, p.dout_ld, p.g, t * kTile, n_rows, buf + kDo, wave, lane);
+    if (wave == 0) {
+      const int r = t * kTile + lane, tok = quot(r, p.g);
+      stat_next = r < n_rows ? stats[static_cast<int64_t>(tok) * p.nh + r - tok * p.g.d] : make_float2(INFINITY, 0.f);
+    }
+  };
+  // the statistics of 64 rows as two arrays, read as broadcasts of 4
+  auto put_stats = [&](uint8_t* buf) {
+    if (wave == 0) {
+      float* s = reinterpret_cast<float*>(buf + kStat);
+      s[lane] = stat_next.x;
+      s[64 + lane] = stat_next.y;
+    }
+  };
+  if (t_first < t_end) load(t_first, smem);
+
+  bf16x8_t kf[S], vf[S];
+  {
+    const int64_t tok = static_cast<int64_t>(st.start) + keyc;
+    const uint16_t* k = p.k + tok * p.k_ld + head * D + 8 * g;
+    const uint16_t* v = p.v + tok * p.v_ld + head * D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < S; ++s) kf[s] = *reinterpret_cast<const bf16x8_t*>(k + 16 * s);
+#pragma unroll
+    for (int s = 0; s < S; ++s) vf[s] = *reinterpret_cast<const bf16x8_t*>(v + 16 * s);
+  }
+  Operands<RB> ops(lane);
+  f32x16_t dk[C], dv[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    dk[c] = f32x16_t{};
+    keep_acc(dk[c]);
+    dv[c] = f32x16_t{};
+    keep_acc(dv[c]);
+  }
+  const float c2 = p.scale * kLog2e;
+
+  auto tile = [&](int t, auto cut_c) {
+    constexpr bool kCut = decltype(cut_c)::value;
+    uint8_t* buf = smem + ((t - t_first) & 1) * kStage;
+    put_stats(buf);                   // the other buffer's readers are a barrier behind
+    wait_vmcnt<0>();
+    lds_barrier();
+    if (t + 1 < t_end) load(t + 1, smem + ((t + 1 - t_first) & 1) * kStage);
+    const float* stat = reinterpret_cast<const float*>(buf + kStat);
+    // 8 S products of two blocks of 32 rows: the scores and dp of block 0, of
+    // block 1, then dv and dk from block 0 and from block 1. Their LDS
+    // operands are read kAhead products ahead, and the element-wise work of
+    // block 0 runs between the products of block 1's scores, that of block 1
+    // between the products of block 0's gradients.
+    constexpr int kB = 2 * S, kN = 4 * kB;
+    bf16x8_t a[kAhead], pf[2][2], sf[2][2];
+    f32x16_t s[2], dp[2];
+    f32x4_t l2[2], dl[2];
+    typedef float f32x8_t __attribute__((ext_vector_type(8)));
+    f32x8_t we, de;                   // elements of the current operand
+    auto fetch = [&](auto n_c) {
+      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+      if constexpr (n < 2 * kB) {
+        constexpr int b = n / kB, k = n % kB;
+        a[slot] = row_operand(smem, ops.row[k / 2] + (k % 2 ? kDo : 0) + b * 32 * RB);
+      } else {
+        constexpr int b = (n - 2 * kB) / kB, k = (n - 2 * kB) % kB / (2 * C), c = (n - 2 * kB) % (2 * C);
+        constexpr int o = (2 * b + k) * 16 * RB + (c < C ? kDo : 0);
+        a[slot] = col_operand(smem, ops.col[c % C][0] + o, ops.col[c % C][1] + o);
+      }
+    };
+    // statistics of 4 rows: elements 4 j .. 4 j + 3 of block b
+    auto stats_of = [&](auto b_c, auto j_c) {
+      constexpr int b = decltype(b_c)::value, j = decltype(j_c)::value;
+      l2[j & 1] = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j + 4 * g);
+      dl[j & 1] = *reinterpret_cast<const f32x4_t*>(stat + 64 + 32 * b + 8 * j + 4 * g);
+    };
+    auto element = [&](auto b_c, auto i_c) {
+      constexpr int b = decltype(b_c)::value, i = decltype(i_c)::value;
+      if constexpr (i % 4 == 0 && i < 12) stats_of(b_c, std::integral_constant<int, i / 4 + 1>{});
+      float w = exp2_hw(fmaf(s[b][i], c2, -l2[(i >> 2) & 1][i & 3]));
+      float d = w * (dp[b][i] - dl[(i >> 2) & 1][i & 3]);
+      if constexpr (kCut) {
+        const bool hidden = t * kTile + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) < row_min;
+        w = hidden ? 0.f : w;
+        d = hidden ? 0.f : d;
+      }
+      we[i % 8] = w;
+      de[i % 8] = d;
+      if constexpr (i % 8 == 7) {
+        pf[b][i / 8] = __builtin_convertvector(we, bf16x8_t);
+        sf[b][i / 8] = __builtin_convertvector(de, bf16x8_t);
+      }
+    };
+    // block b's 16 elements follow its scores at an even pace, all done before
+    // the products that take them
+    auto elements_behind = [&](auto b_c, auto n_c) {
+      constexpr int n = decltype(n_c)::value, b = decltype(b_c)::value;
+      constexpr int from = (b + 1) * kB + 2, room = kB - 4;
+      if constexpr (n >= from && n < from + room) {
+        constexpr int lo = 16 * (n - from) / room, hi = 16 * (n - from + 1) / room;
+        static_for<hi - lo>([&](auto i_c) {
+          element(b_c, std::integral_constant<int, lo + decltype(i_c)::value>{});
+        });
+      }
+    };
+    static_for<kAhead>([&](auto n_c) { fetch(n_c); });
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<kN>([&](auto n_c) {
+      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+      if constexpr (n < 2 * kB) {
+        constexpr int b = n / kB, k = n % kB;
+        if constexpr (k % 2 == 0) s[b] = mfma(a[slot], kf[k / 2], k == 0 ? f32x16_t{} : s[b]);
+        else dp[b] = mfma(a[slot], vf[k / 2], k == 1 ? f32x16_t{} : dp[b]);
+      } else {
+        constexpr int b = (n - 2 * kB) / kB, k = (n - 2 * kB) % kB / (2 * C), c = (n - 2 * kB) % (2 * C);
+        if constexpr (c < C) dv[c] = mfma(a[slot], pf[b][k], dv[c]);
+        else dk[c - C] = mfma(a[slot], sf[b][k], dk[c - C]);
+      }
+      if constexpr (n + kAhead < kN) fetch(std::integral_constant<int, n + kAhead>{});
+      if constexpr (n == kB - 2 || n == 2 * kB - 2)
+        stats_of(std::integral_constant<int, n / kB>{}, std::integral_constant<int, 0>{});
+      elements_behind(std::integral_constant<int, 0>{}, n_c);
+      elements_behind(std::integral_constant<int, 1>{}, n_c);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      keep_acc(dk[c]);
+      keep_acc(dv[c]);
+    }
+    ops.move((t - t_first) & 1 ? -kStage : kStage);
+  };
+  // the tiles that the causal mask cuts come first; each loop has one body
+  const int cut_hi = p.causal ? (first_row(min(k0 + kSide, n_k) - 1) + kTile - 1) / kTile : t_first;
+  const int cut_end = min(t_end, max(t_first, cut_hi));
+  int t = t_first;
+  for (; t < cut_end; ++t) tile(t, std::true_type{});
+  for (; t < t_end; ++t) tile(t, std::false_type{});
+  acc_settled();
+  lds_barrier();                        // everyone is done with the tiles
+  auto value = [&](const f32x16_t& x, int i) {
+    return f32x4_t{read_acc(x[4 * i]), read_acc(x[4 * i + 1]), read_acc(x[4 * i + 2]), read_acc(x[4 * i + 3])};
+  };
+  const int64_t tok = static_cast<int64_t>(st.start) + k0 + wave * 32;
+  const int n_out = n_k - k0 - wave * 32;
+  static_assert(kWaves * result_bytes<RB>() <= 2 * kStage, "results fit the tile buffers");
+  uint8_t* rows = smem + wave * result_bytes<RB>();
+  if (p.parts == 1) {
+    auto put = [&](const f32x16_t* x, float sc, uint16_t* dst, int64_t ld) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4_t y = value(x[c], i) * sc;
+          *reinterpret_cast<uint2*>(rows + (lane & 31) * (RB + 16) + (32 * c + 8 * i + 4 * g) * 2) =
+              pack4(y[0], y[1], y[2], y[3]);
+        }
+      store_rows<RB>(rows, dst + tok * ld + head * D, ld * 2, n_out, lane);
+    };
+    put(dk, p.scale, p.dk, p.dk_ld);
+    put(dv, 1.f, p.dv, p.dv_ld);
+  } else if ((lane & 31) < n_out) {
+    float* dst = p.part + (((static_cast<int64_t>(part) * p.Tk + tok + (lane & 31)) * p.nkv + head) * 2) * D + 4 * g;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<f32x4_t*>(dst + 32 * c + 8 * i) = value(dk[c], i);
+        *reinterpret_cast<f32x4_t*>(dst + D + 32 * c + 8 * i) = value(dv[c], i);
+      }
+  }
+}
+
+// ---- dq: a wave keeps 32 packed rows (the lanes' columns), keys pass by --------
+template <int D>
+__device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index, uint8_t* smem) {
+  constexpr int RB = D * 2, S = D / 16, C = D / 32;
+  constexpr int kV = kTile * RB;                        // V's place behind K's
+  constexpr int kStage = stage_bytes<D>();
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const SeqTile st = find_rows(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, p.g.d, kSide, tile_index);
+  if (st.b < 0) return;
+  const int k_start = st.start2, n_k = st.n2;
+  const int n_rows = st.n, n_q = quot(n_rows, p.g);
+  const int r0 = st.tile * kSide;
+  const int row = r0 + wave * 32 + (lane & 31);
+  const int rowc = row < n_rows ? row : n_rows - 1;
+  const int tok = quot(rowc, p.g), sub = rowc - tok * p.g.d;
+  const int shift = p.causal ? n_k - n_q : n_k;
+  auto last_of = [&](int r) {
+    return p.causal ? min(quot(min(r, n_rows - 1), p.g) + shift, n_k - 1) : n_k - 1;
+  };
+  const int last = p.causal ? min(tok + shift, n_k - 1) : n_k - 1;
+  const int first_last = last_of(r0), tile_last = last_of(r0 + kSide - 1);
+  const int n_kt = tile_last < 0 ? 0 : tile_last / kTile + 1;
+  const int n_full = first_last < 0 ? 0 : min(n_kt, (first_last + 1) / kTile);   // tiles that every row sees whole
+
+  const uint16_t* kb = p.k + static_cast<int64_t>(k_start) * p.k_ld + head * D;
+  const uint16_t* vb = p.v + static_cast<int64_t>(k_start) * p.v_ld + head * D;
+  auto load = [&](int kt, uint8_t* buf) {
+    const int n = n_k - kt * kTile;
+    const int nv = n < kTile ? n : kTile;
+    tile_load<RB, kTile, kWaves>(kb + static_cast<int64_t>(kt) * kTile * p.k_ld, static_cast<uint32_t>(p.k_ld * 2), nv,
+                                 buf, wave, lane);
+    tile_load<RB, kTile, kWaves>(vb + static_cast<int64_t>(kt) * kTile * p.v_ld, static_cast<uint32_t>(p.v_ld * 2), nv,
+                                 buf + kV, wave, lane);
+  };
+  if (n_kt > 0) load(0, smem);
+
+  const int64_t tokc = static_cast<int64_t>(st.start) + tok;
+  const int h = head * p.g.d + sub;
+  bf16x8_t qf[S], df[S];
+  {
+    const uint16_t* q = p.q + tokc * p.q_ld + h * D + 8 * g;
+    const uint16_t* d = p.dout + tokc * p.dout_ld + h * D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < S; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(q + 16 * s);
+#pragma unroll
+    for (int s = 0; s < S; ++s) df[s] = *reinterpret_cast<const bf16x8_t*>(d + 16 * s);
+  }
+  const float2 stat = p.stats[tokc * p.nh + h];
+  Operands<RB> ops(lane);
+  f32x16_t dq[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    dq[c] = f32x16_t{};
+    keep_acc(dq[c]);
+  }
+  const float c2 = p.scale * kLog2e;
+
+  auto tile = [&](int kt, auto cut_c) {
+    constexpr bool kCut = decltype(cut_c)::value;
+    wait_vmcnt<0>();
+    lds_barrier();
+    if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1) & 1) * kStage);
+    // 6 S products, in the order of the kernel above: scores and dp of block 0
+    // and block 1 of 32 keys, then dq from block 0 and from block 1
+    constexpr int kB = 2 * S, kN = 2 * kB + 4 * C;
+    bf16x8_t a[kAhead], sf[2][2];
+    f32x16_t s[2], dp[2];
+    typedef float f32x8_t __attribute__((ext_vector_type(8)));
+    f32x8_t de;
+    auto fetch = [&](auto n_c) {
+      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+      if constexpr (n < 2 * kB) {
+        constexpr int b = n / kB, k = n % kB;
+        a[slot] = row_operand(smem, ops.row[k / 2] + (k % 2 ? kV : 0) + b * 32 * RB);
+      } else {
+        constexpr int k = (n - 2 * kB) / C, c = (n - 2 * kB) % C;
+        a[slot] = col_operand(smem, ops.col[c][0] + k * 16 * RB, ops.col[c][1] + k * 16 * RB);
+      }
+    };
+    auto element = [&](auto b_c, auto i_c) {
+      constexpr int b = decltype(b_c)::value, i = decltype(i_c)::value;
+      float d = exp2_hw(fmaf(s[b][i], c2, -stat.x)) * (dp[b][i] - stat.y);
+      if constexpr (kCut) d = kt * kTile + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) > last ? 0.f : d;
+      de[i % 8] = d;
+      if constexpr (i % 8 == 7) sf[b][i / 8] = __builtin_convertvector(de, bf16x8_t);
+    };
+    // elements [8 part, 8 part + 8) of block b behind products [from, from + room)
+    auto elements_behind = [&](auto b_c, auto part_c, auto from_c, auto room_c, auto n_c) {
+      constexpr int n = decltype(n_c)::value, from = decltype(from_c)::value, room = decltype(room_c)::value;
+      if constexpr (n >= from && n < from + room) {
+        constexpr int lo = 8 * (n - from) / room, hi = 8 * (n - from + 1) / room;
+        static_for<hi - lo>([&](auto i_c) {
+          element(b_c, std::integral_constant<int, 8 * decltype(part_c)::value + lo + decltype(i_c)::value>{});
+        });
+      }
+    };
+    static_for<kAhead>([&](auto n_c) { fetch(n_c); });
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<kN>([&](auto n_c) {
+      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
+      if constexpr (n < 2 * kB) {
+        constexpr int b = n / kB, k = n % kB;
+        if constexpr (k % 2 == 0) s[b] = mfma(a[slot], qf[k / 2], k == 0 ? f32x16_t{} : s[b]);
+        else dp[b] = mfma(a[slot], df[k / 2], k == 1 ? f32x16_t{} : dp[b]);
+      } else {
+        constexpr int k = (n - 2 * kB) / C, c = (n - 2 * kB) % C;
+        dq[c] = mfma(a[slot], sf[k / 2][k % 2], dq[c]);
+      }
+      if constexpr (n + kAhead < kN) fetch(std::integral_constant<int, n + kAhead>{});
+      typedef std::integral_constant<int, 0> I0;
+      typedef std::integral_constant<int, 1> I1;
+      // block 0 behind block 1's scores; block 1's two halves each before
+      // their own products (k-steps 2 and 3)
+      constexpr int kHalf = kB / 2 - 1;
+      elements_behind(I0{}, I0{}, std::integral_constant<int, kB + 2>{}, std::integral_constant<int, kHalf>{}, n_c);
+      elements_behind(I0{}, I1{}, std::integral_constant<int, kB + 2 + kHalf>{},
+                      std::integral_constant<int, kB - 2 - kHalf>{}, n_c);
+      elements_behind(I1{}, I0{}, std::integral_constant<int, 2 * kB + 2 * C - (2 * C - 1)>{},
+                      std::integral_constant<int, 2 * C - 1>{}, n_c);
+      elements_behind(I1{}, I1{}, std::integral_constant<int, 2 * kB + 2 * C>{}, std::integral_constant<int, C>{},
+                      n_c);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+#pragma unroll
+    for (int c = 0; c < C; ++c) keep_acc(dq[c]);
+    ops.move(kt & 1 ? -kStage : kStage);
+  };
+  int kt = 0;
+  for (; kt < n_full; ++kt) tile(kt, std::false_type{});
+  for (; kt < n_kt; ++kt) tile(kt, std::true_type{});
+
+  acc_settled();
+  lds_barrier();                        // everyone is done with the tiles
+  uint8_t* rows = smem + wave * result_bytes<RB>();
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float sc = p.scale;
+      *reinterpret_cast<uint2*>(rows + (lane & 31) * (RB + 16) + (32 * c + 8 * i + 4 * g) * 2) =
+          pack4(read_acc(dq[c][4 * i]) * sc, read_acc(dq[c][4 * i + 1]) * sc, read_acc(dq[c][4 * i + 2]) * sc,
+                read_acc(dq[c][4 * i + 3]) * sc);
+    }
+  store_packed<RB>(rows, p.dq + static_cast<int64_t>(st.start) * p.dq_ld + head * p.g.d * D, p.dq_ld, p.g,
+                   r0 + wave * 32, n_rows, lane);
+}
+
+// Both kinds in one launch, dk / dv first: the second fills the compute units
+// that the first's last workgroups leave. Heads run fastest (an XCD keeps to
+// its own where their number is a multiple of 8); the tiles that see most come
+// first.
+template <int D>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void bwd_kernel(BwdArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * stage_bytes<D>()];
+  const int n_kv = p.k_tiles * p.nkv * p.parts;
+  const int id = blockIdx.x;
+  const int head = id % p.nkv;
+  if (id < n_kv) {
+    const int r = id / p.nkv;
+    bwd_kv<D>(p, head, r % p.parts, r / p.parts, smem);
+  } else {
+    bwd_q<D>(p, head, p.q_tiles - 1 - (id - n_kv) / p.nkv, smem);
+  }
+}
+
+// ---- dk, dv: the parts' sum, in order ------------------------------------------
+// Only rows that a sequence holds.
+template <int D>
+__global__ __launch_bounds__(256) void bwd_join_kernel(BwdArgs p) {
+  const int lo = clamp_int(p.cu_k[0], 0, p.Tk), hi = clamp_int(p.cu_k[p.B], lo, p.Tk);
+  constexpr int kL = 2 * D / 4;                          // lanes a (token, head)
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (256 / kL) + threadIdx.x / kL;
+  const int64_t t = unit / p.nkv;
+  const int head = static_cast<int>(unit - t * p.nkv);
+  if (t < lo || t >= hi) return;
+  const int c = (threadIdx.x & (kL - 1)) * 4;            // of (dk | dv)
+  const float* src = p.part + unit * 2 * D + c;
+  const int64_t step = static_cast<int64_t>(p.Tk) * p.nkv * 2 * D;
+  f32x4_t s = *reinterpret_cast<const f32x4_t*>(src);
+#pragma unroll 4
+  for (int i = 1; i < p.parts; ++i) {
+    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(src + i * step);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] += x[j];
+  }
+  if (c < D)
+    *reinterpret_cast<uint2*>(p.dk + t * p.dk_ld + head * D + c) =
+        pack4(s[0] * p.scale, s[1] * p.scale, s[2] * p.scale, s[3] * p.scale);
+  else
+    *reinterpret_cast<uint2*>(p.dv + t * p.dv_ld + head * D + c - D) = pack4(s[0], s[1], s[2], s[3]);
+}
+
+// Parts that the rows of a key tile are cut into: enough workgroups for two a
+// compute unit, as far as a part keeps 4 tiles of rows in the mean.
+int parts_of(int Tq, int Tk, int nh, int nkv) {
+  const int64_t wgs = (static_cast<int64_t>(Tk) + kSide - 1) / kSide * nkv;
+  const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (4 * kTile);
+  int64_t n = 2 * kNumCu / (wgs > 0 ? wgs : 1);
+  n = n < tiles ? n : tiles;
+  return n < 1 ? 1 : (n > 16 ? 16 : static_cast<int>(n));
+}
+// Rows of the parts' sums: parts_of never brings them above either bound, and
+// both grow with the sizes, so a workspace serves every smaller call.
+size_t part_rows(int Tk, int nkv) {
+  const size_t all = size_t{16} * Tk * nkv, most = size_t{2} * kNumCu * kSide;
+  return all < most ? all : most;
+}
+size_t stats_bytes(int Tq, int nh) { return (static_cast<size_t>(Tq) * nh * 8 + 255) & ~size_t{255}; }
+
+template <int D>
+void launch_bwd(const BwdArgs& a, hipStream_t stream) {
+  if (a.Tq > 0) {
+    const int64_t rows = static_cast<int64_t>(a.Tq) * a.nh;
+    constexpr int kPer = 256 / (D / 8);
+    hipLaunchKernelGGL(bwd_stats_kernel<D>, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)), dim3(256), 0, stream,
+                       a);
+  }
+  hipLaunchKernelGGL(bwd_kernel<D>, dim3(static_cast<unsigned>(a.k_tiles * a.parts + a.q_tiles) * a.nkv),
+                     dim3(64 * kWaves), 0, stream, a);
+  if (a.parts > 1) {
+    constexpr int kPer = 256 / (D / 2);
+    const int64_t units = static_cast<int64_t>(a.Tk) * a.nkv;
+    hipLaunchKernelGGL(bwd_join_kernel<D>, dim3(static_cast<unsigned>((units + kPer - 1) / kPer)), dim3(256), 0,
+                       stream, a);
+  }
+}
+
+}  // namespace
+}  // namespace gqa
+}  // namespace moe
+
+extern "C" size_t moe_gqa_attn_bwd_workspace(int Tq, int Tk, int n_heads, int n_kv_heads, int head_dim) {
+  if (Tq < 0 || Tk < 0 || Tq > (1 << 27) || Tk > (1 << 27) || n_heads < 1 || n_heads > 1024 || n_kv_heads < 1 ||
+      n_heads % n_kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return moe::gqa::stats_bytes(Tq, n_heads) + moe::gqa::part_rows(Tk, n_kv_heads) * 2 * head_dim * 4;
+}
+
+extern "C" int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q_ld, const void* k,
+                                int64_t k_ld, const void* v, int64_t v_ld, int fmt, const void* out, int64_t out_ld,
+                                const float* lse, const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk,
+                                int n_heads, int n_kv_heads, int head_dim, int causal, float scale, void* dq,
+                                int64_t dq_ld, void* dk, int64_t dk_ld, void* dv, int64_t dv_ld, void* ws,
+                                size_t ws_bytes, hipStream_t stream) {
+  using namespace moe;
+  using namespace moe::gqa;
+  clear_error();
+  const char* fn = "moe_gqa_attn_bwd";
+  if (const int rc = check_heads(fn, fmt, n_heads, n_kv_heads, head_dim)) return rc;
+  if (const int rc = check_sequences(fn, B, Tq, Tk, n_heads, causal, scale)) return rc;
+  const int64_t q_row = static_cast<int64_t>(n_heads) * head_dim, k_row = static_cast<int64_t>(n_kv_heads) * head_dim;
+  const struct { const char* name; int64_t ld, row; } lds[] = {
+      {"dout_ld", dout_ld, q_row}, {"q_ld", q_ld, q_row}, {"k_ld", k_ld, k_row}, {"v_ld", v_ld, k_row},
+      {"out_ld", out_ld, q_row}, {"dq_ld", dq_ld, q_row}, {"dk_ld", dk_ld, k_row}, {"dv_ld", dv_ld, k_row}};
+  for (const auto& x : lds)
+    if (const int rc = check_ld(fn, x.name, x.ld, x.row)) return rc;
+  if (B == 0 || (Tq == 0 && Tk == 0)) return MOE_OK;
+  MOE_REQUIRE(cu_q && cu_k && (Tq == 0 || (dout && q && out && lse && dq)) && (Tk == 0 || (k && v && dk && dv)),
+              MOE_ERR_INVALID_ARG, "moe_gqa_attn_bwd: null pointer");
+  MOE_REQUIRE(aligned16(dout) && aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out) && aligned16(dq) &&
+                  aligned16(dk) && aligned16(dv) && aligned16(ws),
+              MOE_ERR_ALIGNMENT, "moe_gqa_attn_bwd: tensors and ws must be 16-byte aligned");
+  const size_t need = moe_gqa_attn_bwd_workspace(Tq, Tk, n_heads, n_kv_heads, head_dim);
+  MOE_REQUIRE(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE,
+              "moe_gqa_attn_bwd: ws smaller than moe_gqa_attn_bwd_workspace(...)");
+  BwdArgs a{};
+  a.dout = static_cast<const uint16_t*>(dout), a.dout_ld = dout_ld;
+  a.q = static_cast<const uint16_t*>(q), a.q_ld = q_ld;
+  a.k = static_cast<const uint16_t*>(k), a.k_ld = k_ld;
+  a.v = static_cast<const uint16_t*>(v), a.v_ld = v_ld;
+  a.out = static_cast<const uint16_t*>(out), a.out_ld = out_ld;
+  a.lse = lse, a.cu_q = cu_q, a.cu_k = cu_k;
+  a.B = B, a.Tq = Tq, a.Tk = Tk, a.nh = n_heads, a.nkv = n_kv_heads, a.causal = causal, a.scale = scale;
+  a.g = make_div(n_heads / n_kv_heads);
+  a.dq = static_cast<uint16_t*>(dq), a.dq_ld = dq_ld;
+  a.dk = static_cast<uint16_t*>(dk), a.dk_ld = dk_ld;
+  a.dv = static_cast<uint16_t*>(dv), a.dv_ld = dv_ld;
+  a.stats = static_cast<float2*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + stats_bytes(Tq, n_heads));
+  a.parts = parts_of(Tq, Tk, n_heads, n_kv_heads);
+  a.k_tiles = Tk > 0 ? Tk / kSide + (B < Tk ? B : Tk) : 0;
+  a.q_tiles = Tq > 0 ? Tq * a.g.d / kSide + (B < Tq ? B : Tq) : 0;
+  if (head_dim == 128) launch_bwd<128>(a, stream);
+  else launch_bwd<64>(a, stream);
+  return check_launch(fn);
+}

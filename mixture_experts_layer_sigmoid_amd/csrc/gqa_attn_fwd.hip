@@ -1,0 +1,218 @@
+// moe_gqa_attn_fwd: attention over packed sequences, grouped heads.
+//
+// Per query head h of key head h / G and packed sequence:
+//   s[i, j] = scale * q[i, h] . k[j, h / G]
+//   out[i, h] = sum_j softmax_j(s[i, :]) v[j, h / G],  lse[i, h] = log sum_j e^s
+// over the keys the mask leaves; a row without keys has out 0 and lse -inf.
+//
+// One pass over the keys with a running reference and sum (fp32). A wave keeps
+// 32 packed rows (tokens x heads of a group) as the columns of its
+// accumulators: the scores are computed as k q^T, so a row's statistics belong
+// to one lane and its mirror, and the weights in the accumulator are the next
+// product's operand without moving. The weights are rounded to bf16, as the
+// matrix instruction takes them; their sum is taken before that rounding.
+#include "gqa.h"
+
+#include <cmath>
+
+namespace moe {
+namespace gqa {
+namespace {
+
+struct FwdArgs {
+  const uint16_t* q;
+  int64_t q_ld;
+  const uint16_t* k;
+  int64_t k_ld;
+  const uint16_t* v;
+  int64_t v_ld;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int B, Tq, Tk, nh, nkv, causal;
+  Div g;
+  float scale;
+  uint16_t* out;
+  int64_t out_ld;
+  float* lse;
+  int n_tiles;
+};
+
+constexpr int kKt = 64;                                  // keys per tile
+constexpr int NW = 4;                                    // waves, 32 rows each
+
+template <int D>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void attn_fwd_kernel(FwdArgs p) {
+  constexpr int kQt = 32 * NW;
+  constexpr int RB = D * 2;
+  constexpr int kTileK = kKt * RB, kTileBytes = 2 * kTileK;
+  constexpr int kRows = NW * result_bytes<RB>();
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kTileBytes > kRows ? 2 * kTileBytes : kRows];
+  const int lane = threadIdx.x & 63, g = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // heads run fastest: workgroups go to the XCDs in turn, so with 8 key heads
+  // (or a multiple) an XCD keeps to its own; later tiles of a sequence see
+  // more keys and come first
+  const int head = blockIdx.x % p.nkv;
+  const SeqTile st = find_rows(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, p.g.d, kQt, p.n_tiles - 1 - blockIdx.x / p.nkv);
+  if (st.b < 0) return;
+  const int k_start = st.start2, n_k = st.n2;
+  const int n_rows = st.n, n_q = quot(n_rows, p.g);
+
+  const int r0 = st.tile * kQt + wave * 32;
+  const int row = r0 + (lane & 31);                              // within the sequence
+  const int rowc = row < n_rows ? row : n_rows - 1;
+  const int tok = quot(rowc, p.g), sub = rowc - tok * p.g.d;
+  // last visible key of this lane's row, and of the wave's and the tile's
+  const int shift = p.causal ? n_k - n_q : n_k;
+  auto last_of = [&](int r) {
+    return p.causal ? min(quot(min(r, n_rows - 1), p.g) + shift, n_k - 1) : n_k - 1;
+  };
+  const int last = p.causal ? min(tok + shift, n_k - 1) : n_k - 1;
+  const int wave_first = last_of(r0), wave_last = last_of(r0 + 31);
+  const int tile_last = last_of(st.tile * kQt + kQt - 1);
+  const int n_kt = tile_last < 0 ? 0 : tile_last / kKt + 1;
+
+  const uint16_t* kb = p.k + static_cast<int64_t>(k_start) * p.k_ld + head * D;
+  const uint16_t* vb = p.v + static_cast<int64_t>(k_start) * p.v_ld + head * D;
+  auto load = [&](int kt, uint8_t* buf) {
+    const int n = n_k - kt * kKt;
+    const int nv = n < kKt ? n : kKt;
+    tile_load<RB, kKt, NW>(kb + static_cast<int64_t>(kt) * kKt * p.k_ld, static_cast<uint32_t>(p.k_ld * 2), nv, buf,
+                           wave, lane);
+    tile_load<RB, kKt, NW>(vb + static_cast<int64_t>(kt) * kKt * p.v_ld, static_cast<uint32_t>(p.v_ld * 2), nv,
+                           buf + kTileK, wave, lane);
+  };
+  if (n_kt > 0) load(0, smem);
+
+  bf16x8_t qf[D / 16];
+  {
+    const uint16_t* q = p.q + (static_cast<int64_t>(st.start) + tok) * p.q_ld + (head * p.g.d + sub) * D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(q + 16 * s);
+  }
+  uint32_t k_off[D / 16], v_off[D / 32][2];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) k_off[s] = row_operand_offset<RB>(lane, s);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v_off[c][h] = kTileK + col_operand_offset<RB>(lane, c, h);
+
+  f32x16_t o[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) o[c] = f32x16_t{};
+  float m = -INFINITY, l = 0.f;
+  const float c2 = p.scale * kLog2e;
+
+  for (int kt = 0; kt < n_kt; ++kt) {
+    wait_vmcnt<0>();
+    lds_barrier();
+    uint8_t* buf = smem + (kt & 1) * kTileBytes;
+    if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1) & 1) * kTileBytes);
+    const int t0 = kt * kKt;
+    if (t0 > wave_last) continue;          // nothing of this tile is visible to the wave
+    f32x16_t s[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      s[b] = f32x16_t{};
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) s[b] = mfma(row_operand(buf, k_off[k] + b * 32 * RB), qf[k], s[b]);
+    }
+    if (t0 + kKt - 1 > wave_first) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (t0 + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) > last) s[b][i] = -INFINITY;
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+    mx = fmaxf(mx, other_half(mx));
+    const float mn = next_ref(m, mx, c2);
+    // a row that has seen no key yet keeps the maximum -inf: its exponents
+    // are taken against 0, so every weight is 2^-inf = 0 and not NaN
+    const float mc = mn == -INFINITY ? 0.f : mn * c2;
+    if (__any(mn > m)) {
+      const float a = exp2_hw(fmaf(m, c2, -mc));
+      l *= a;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[c][i] *= a;
+      m = mn;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = exp2_hw(fmaf(s[b][i], c2, -mc));
+        sum += s[b][i];
+      }
+    l += sum;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bf16x8_t pf = pack_operand(s[b], k);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          o[c] = mfma(col_operand(buf, v_off[c][0] + (2 * b + k) * 16 * RB, v_off[c][1] + (2 * b + k) * 16 * RB), pf,
+                      o[c]);
+      }
+  }
+  l += other_half(l);
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  lds_barrier();                        // everyone is done with the tiles
+  uint8_t* rows = smem + wave * result_bytes<RB>();
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint2*>(rows + (lane & 31) * (RB + 16) + (32 * c + 8 * i + 4 * g) * 2) =
+          pack4(o[c][4 * i] * inv, o[c][4 * i + 1] * inv, o[c][4 * i + 2] * inv, o[c][4 * i + 3] * inv);
+  store_packed<RB>(rows, p.out + static_cast<int64_t>(st.start) * p.out_ld + head * p.g.d * D, p.out_ld, p.g, r0,
+                   n_rows, lane);
+  if (p.lse && g == 0 && row < n_rows)
+    p.lse[(static_cast<int64_t>(st.start) + tok) * p.nh + head * p.g.d + sub] =
+        l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
+}
+
+}  // namespace
+}  // namespace gqa
+}  // namespace moe
+
+extern "C" int moe_gqa_attn_fwd(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                                int fmt, const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk, int n_heads,
+                                int n_kv_heads, int head_dim, int causal, float scale, void* out, int64_t out_ld,
+                                float* lse, hipStream_t stream) {
+  using namespace moe;
+  using namespace moe::gqa;
+  clear_error();
+  const char* fn = "moe_gqa_attn_fwd";
+  if (const int rc = check_heads(fn, fmt, n_heads, n_kv_heads, head_dim)) return rc;
+  if (const int rc = check_sequences(fn, B, Tq, Tk, n_heads, causal, scale)) return rc;
+  const int64_t q_row = static_cast<int64_t>(n_heads) * head_dim, k_row = static_cast<int64_t>(n_kv_heads) * head_dim;
+  if (const int rc = check_ld(fn, "q_ld", q_ld, q_row)) return rc;
+  if (const int rc = check_ld(fn, "k_ld", k_ld, k_row)) return rc;
+  if (const int rc = check_ld(fn, "v_ld", v_ld, k_row)) return rc;
+  if (const int rc = check_ld(fn, "out_ld", out_ld, q_row)) return rc;
+  if (B == 0 || Tq == 0) return MOE_OK;
+  MOE_REQUIRE(q && cu_q && cu_k && out && (Tk == 0 || (k && v)), MOE_ERR_INVALID_ARG,
+              "moe_gqa_attn_fwd: null pointer");
+  MOE_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out), MOE_ERR_ALIGNMENT,
+              "moe_gqa_attn_fwd: q, k, v and out must be 16-byte aligned");
+  FwdArgs a{static_cast<const uint16_t*>(q), q_ld, static_cast<const uint16_t*>(k), k_ld,
+            static_cast<const uint16_t*>(v), v_ld, cu_q, cu_k, B, Tq, Tk, n_heads, n_kv_heads, causal,
+            make_div(n_heads / n_kv_heads), scale, static_cast<uint16_t*>(out), out_ld, lse, 0};
+  a.n_tiles = Tq * a.g.d / (32 * NW) + (B < Tq ? B : Tq);
+  const dim3 grid(static_cast<unsigned>(a.n_tiles) * n_kv_heads);
+  if (head_dim == 128) hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(64 * NW), 0, stream, a);
+  else hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(64 * NW), 0, stream, a);
+  return check_launch(fn);
+}
