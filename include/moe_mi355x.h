@@ -932,9 +932,9 @@ int moe_gqa_append(const void* k, int64_t k_ld, const void* v, int64_t v_ld, int
                    const int32_t* lens, const int32_t* cu, int B, int T, int n_kv_heads,
                    int head_dim, hipStream_t stream);
 
-/* moe_gqa_decode_workspace — bytes of moe_gqa_decode's workspace for up to T
- * new tokens of up to B requests (it grows with both; 0 for bad sizes). */
-size_t moe_gqa_decode_workspace(int B, int T, int n_heads, int n_kv_heads, int head_dim);
+/* moe_gqa_decode_workspace — bytes of moe_gqa_decode's workspace, for calls of
+ * any size (0 for a bad head_dim). */
+size_t moe_gqa_decode_workspace(int head_dim);
 
 /*
  * moe_gqa_decode — attention of the last tokens of B requests over the cache
@@ -951,7 +951,10 @@ size_t moe_gqa_decode_workspace(int B, int T, int n_heads, int n_kv_heads, int h
  * What the cache holds behind a request's length is never used, and NaN codes
  * of tokens that a new token does not see do not reach it. A token that sees
  * nothing gives out 0 and lse -inf.
- * ws       moe_gqa_decode_workspace(B, T, ...) bytes.
+ * ws       moe_gqa_decode_workspace(head_dim) bytes, filled with zeros once
+ *          before the first call that takes it; every call leaves it ready for
+ *          the next, of any size. Calls that may run at the same time need one
+ *          each.
  */
 int moe_gqa_decode(const void* q, int64_t q_ld, int fmt, const void* k_cache,
                    const void* v_cache, const uint8_t* k_scales, const uint8_t* v_scales,

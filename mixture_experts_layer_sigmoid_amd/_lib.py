@@ -79,7 +79,7 @@ SIGNATURES = {
                               _I, _I, _I, _I, _F, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P]),
     "moe_gqa_append": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I,
                             _P]),
-    "moe_gqa_decode_workspace": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_gqa_decode_workspace": (_SZ, [_I]),
     "moe_gqa_decode": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I,
                             _F, _P, _I64, _P, _P, _SZ, _P]),
     "moe_grouped_mlp_bwd_workspace": (_SZ, [_I, _I, _I, _I, _I, _I64, _I]),
@@ -438,8 +438,8 @@ def moe_gqa_append(k, k_ld, v, v_ld, fmt, k_cache, v_cache, k_scales, v_scales, 
         _stream(stream)))
 
 
-def moe_gqa_decode_workspace(B, T, n_heads, n_kv_heads, head_dim) -> int:
-    return load().moe_gqa_decode_workspace(B, T, n_heads, n_kv_heads, head_dim)
+def moe_gqa_decode_workspace(head_dim) -> int:
+    return load().moe_gqa_decode_workspace(head_dim)
 
 
 def moe_gqa_decode(q, q_ld, fmt, k_cache, v_cache, k_scales, v_scales, page_size, n_pages, page_table,

@@ -6,14 +6,15 @@
 // over the tokens that it sees. The group's heads of a request's new tokens
 // are the packed rows of one product over the head's cache, 32 at a time.
 //
-// Two launches. Attention: the cached tokens of each (request, key head, 32
-// rows) are cut into pieces of about equal length, one workgroup each, whose
-// four waves take 32 tokens in turn. A wave reads keys and values straight
-// into registers (the cache lies in operand order), a tile ahead of its
-// products, and turns codes into bf16 operands with the block's scale in the
-// same instruction, exactly. So nothing passes LDS and no wave waits for
-// another before the piece's end, where the four sums are added in order. The
-// join adds the pieces in order; a row that one piece covers is stored at once.
+// One launch. The cached tokens of each (request, key head, 32 rows) are cut
+// into pieces of about equal length, one workgroup each, whose four waves take
+// 32 tokens in turn. A wave reads keys and values straight into registers (the
+// cache lies in operand order), a tile ahead of its products, and turns codes
+// into bf16 operands with the block's scale in the same instruction, exactly.
+// So nothing passes LDS and no wave waits for another before the piece's end,
+// where the four sums are added in order. Pieces meet in the workspace: the
+// workgroup that finishes a segment's last piece adds them, in their order
+// whichever it is, so results repeat bit for bit.
 //
 // Roundings: the weights to bf16 as operands (their sum is taken before that).
 // Codes times scales are exact in bf16; scores and all sums are fp32.
@@ -28,8 +29,11 @@ namespace {
 constexpr int kTok = 32;                               // cached tokens a tile
 constexpr int NW = 4;                                  // waves a workgroup
 constexpr int kRows = 32;                              // packed rows a workgroup
-constexpr int kPieces = 512;                           // pieces beside one a (request, head, rows)
-constexpr int kLeast = NW;                             // tiles a piece, at least
+constexpr int kPieces = 2 * kNumCu;                    // pieces beside one a (request, head, rows)
+constexpr int kParts = 2 * kPieces;                    // pieces of segments that have several, at most
+constexpr int kLeast = 4 * NW;                         // tiles a piece, at least
+constexpr int kAlone = 8 * NW;                         // tiles that are not cut
+constexpr int kJoin = 16;                              // neighbouring pieces that are joined first
 
 struct DecodeArgs {
   const uint16_t* q;
@@ -51,19 +55,11 @@ struct DecodeArgs {
   uint16_t* out;
   int64_t out_ld;
   float* lse;
-  float* part;               // [workgroups, 32, D]: pieces, not normalized
-  float2* part_ml;           // [workgroups, 32]: their (reference, sum)
-  int wgs;                   // workgroups that part has room for
-};
-
-// A request's part of the work.
-struct Seg {
-  int b;                     // -1: none
-  int start, n_q, len;       // rows of q, new tokens, cached tokens
-  int tiles, pieces;         // of a (head, 32 rows)
-  int row_tiles;
-  int rest;                  // workgroup (or segment) within the request
-  int first;                 // first workgroup of the request
+  float* part;               // [kParts, 32, D]: pieces of segments that have several, not normalized
+  float2* part_ml;           // [kParts, 32]: their (reference, sum)
+  int* done;                 // [2, kParts]: pieces of a group, and groups of a segment, that are in place;
+                             // at the first piece's place; zero between calls
+  int segs;                  // segments that the grid has room for
 };
 
 // What each lane knows of one request.
@@ -79,38 +75,58 @@ __device__ __forceinline__ void request(const DecodeArgs& p, int b, int* start, 
   *row_tiles = (*n_q * p.g.d + kRows - 1) / kRows;
 }
 
-// Tiles of a piece: all tiles over kPieces workgroups, at least kLeast.
-__device__ __forceinline__ int piece_tiles(const DecodeArgs& p) {
-  const int lane = threadIdx.x & 63;
-  int64_t all = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    int s, n, len, tiles, rt;
-    request(p, b0 + lane, &s, &n, &len, &tiles, &rt);
-    all += static_cast<int64_t>(tiles) * rt * p.nkv;
-  }
+// Tiles of a piece: at least all tiles over kPieces (so fewer than kPieces
+// segments have several pieces, and those fewer than 2 kPieces pieces), and at
+// least kLeast. all, segs: one lane's share of the call's tiles and segments.
+__device__ __forceinline__ int piece_tiles(const DecodeArgs& p, int64_t all, int64_t segs) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) all += __shfl_xor(all, o, 64);
-  const int64_t c = (all + kPieces - 1) / kPieces;
+  for (int o = 32; o >= 1; o >>= 1) {
+    all += __shfl_xor(all, o, 64);
+    segs += __shfl_xor(segs, o, 64);
+  }
+  // requests whose rows overlap can exceed the grid: then nothing is cut
+  if (segs > p.segs) return 1 << 30;
+  // two workgroups fill a compute unit: while the segments leave room, all
+  // pieces run at once
+  const int64_t n = segs >= kPieces ? kPieces : (segs > kPieces / 2 ? kPieces / 2 : kPieces - segs);
+  const int64_t c = (all + n - 1) / n;
   return c > kLeast ? static_cast<int>(c < (1 << 30) ? c : (1 << 30)) : kLeast;
 }
 
-// Workgroup `index` (by_piece) or segment (request, head, rows) `index` of the
-// call. The pieces of a request run slowest, its 32-row tiles fastest, so
-// neighbours read the same tokens.
-__device__ __forceinline__ Seg find_work(const DecodeArgs& p, int index, bool by_piece) {
+// A workgroup's part of the work.
+struct Seg {
+  int b;                     // -1: none
+  int start, n_q, len;       // rows of q, new tokens, cached tokens
+  int tiles, pieces;         // of a (head, 32 rows)
+  int row_tiles;
+  int rest;                  // workgroup within the request
+  int part;                  // the request's first place in part
+};
+
+// The pieces of a request run slowest, its 32-row tiles fastest, so neighbours
+// read the same tokens.
+__device__ __forceinline__ Seg find_work(const DecodeArgs& p, int index) {
   const int lane = threadIdx.x & 63;
-  const int c = piece_tiles(p);
-  int64_t before = 0, wgs = 0;
+  int64_t all = 0, segs = 0;
+  int s, n, len, tiles, rt;
   for (int b0 = 0; b0 < p.B; b0 += 64) {
-    int s, n, len, tiles, rt;
     request(p, b0 + lane, &s, &n, &len, &tiles, &rt);
-    const int pieces = tiles > c ? (tiles + c - 1) / c : 1;
-    const int seg = rt * p.nkv, groups = seg * pieces, count = by_piece ? groups : seg;
-    int sum = count, gsum = groups;
+    all += static_cast<int64_t>(tiles) * rt * p.nkv;
+    segs += rt * p.nkv;
+  }
+  const int c = piece_tiles(p, all, segs);
+  int64_t before = 0;
+  int parts = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 64) {
+    if (p.B > 64) request(p, b0 + lane, &s, &n, &len, &tiles, &rt);   // else they are at hand
+    const int pieces = tiles > c && tiles > kAlone ? (tiles + c - 1) / c : 1;
+    const int seg = rt * p.nkv, groups = seg * pieces;
+    const int cut = pieces > 1 ? seg : 0;
+    int sum = groups, psum = cut * pieces;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(sum, o, 64), w = __shfl_up(gsum, o, 64);
-      if (lane >= o) sum += u, gsum += w;
+      const int u = __shfl_up(sum, o, 64), v = __shfl_up(psum, o, 64);
+      if (lane >= o) sum += u, psum += v;
     }
     const uint64_t hit = __ballot(before + sum > index);
     if (hit) {
@@ -123,14 +139,20 @@ __device__ __forceinline__ Seg find_work(const DecodeArgs& p, int index, bool by
       r.tiles = __builtin_amdgcn_readlane(tiles, l);
       r.pieces = __builtin_amdgcn_readlane(pieces, l);
       r.row_tiles = __builtin_amdgcn_readlane(rt, l);
-      r.rest = static_cast<int>(index - before) - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(count, l));
-      r.first = static_cast<int>(wgs) + __builtin_amdgcn_readlane(gsum, l) - __builtin_amdgcn_readlane(groups, l);
+      r.rest = static_cast<int>(index - before) - __builtin_amdgcn_readlane(sum - groups, l);
+      r.part = parts + __builtin_amdgcn_readlane(psum - cut * pieces, l);
       return r;
     }
     before += __builtin_amdgcn_readlane(sum, 63);
-    wgs += __builtin_amdgcn_readlane(gsum, 63);
+    parts += __builtin_amdgcn_readlane(psum, 63);
   }
   return Seg{-1, 0, 0, 0, 0, 0, 0, 0, 0};
+}
+
+// Workgroups go to the XCDs in turn; runs of 8 work items stay on one, whose
+// L2 then serves the row tiles that read the same tokens.
+__device__ __forceinline__ int runs_of_8(int id, int n) {
+  return id < (n & ~63) ? (id & ~63) + (id & 7) * 8 + ((id >> 3) & 7) : id;
 }
 
 // 8 codes times a scale as a bf16 operand
@@ -148,6 +170,97 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 }
 __device__ __forceinline__ float scale_of(int byte) { return __uint_as_float(static_cast<uint32_t>(byte) << 23); }
 
+// Pieces pass between compute units of different XCDs, whose L2 caches do not
+// see each other's lines: device-scope accesses go past them. (Fences instead
+// would write back and drop whole L2 caches under the other workgroups' loads:
+// 81 against 32 us for 8 long caches.)
+__device__ __forceinline__ void put2(void* to, float a, float b) {
+  const uint64_t v = static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+  __hip_atomic_store(static_cast<uint64_t*>(to), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get2(const void* from) {
+  const uint64_t v = __hip_atomic_load(static_cast<const uint64_t*>(from), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+
+// Whether this workgroup is the last of n to arrive at a counter; all its
+// stores have arrived before it counts. The last one leaves zero.
+__device__ __forceinline__ bool last_of(int* count, int n, int* flag) {
+  wait_vmcnt<0>();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int k = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (k == n - 1) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = k == n - 1;
+  }
+  __syncthreads();
+  return *flag;
+}
+
+// Sum of n pieces, `step` places apart from place `at`, in order: D / 4 lanes a
+// row, put(row, first value, sums, reference, sum of weights). U units (rows a
+// lane) and K pieces are asked for at once.
+template <int D, int U, int K, typename Put>
+__device__ __forceinline__ void join_units(const DecodeArgs& p, float c2, int n_out, int at, int n, int step,
+                                           Put&& put) {
+  constexpr int kL = D / 4, kPer = 64 / kL;            // lanes a row, rows a wave
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int d = lane % kL * 4;
+  f32x4_t x[U];
+  float ref[U], sum[U];
+  const float2* pm[U];
+  const float* px[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = min((u * NW + wave) * kPer + lane / kL, n_out - 1);
+    pm[u] = p.part_ml + static_cast<int64_t>(at) * kRows + r;
+    px[u] = p.part + (static_cast<int64_t>(at) * kRows + r) * D + d;
+    x[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    ref[u] = -INFINITY, sum[u] = 0.f;
+  }
+  for (int i0 = 0; i0 < n; i0 += K) {
+    float2 y[U][K], z0[U][K], z1[U][K];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const int64_t o = static_cast<int64_t>(min(i0 + i, n - 1)) * step * kRows;
+        y[u][i] = get2(pm[u] + o);
+        z0[u][i] = get2(px[u] + o * D);
+        z1[u][i] = get2(px[u] + o * D + 2);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float top = ref[u];
+#pragma unroll
+      for (int i = 0; i < K; ++i) top = fmaxf(top, y[u][i].x);
+      const float tc = top == -INFINITY ? 0.f : top * c2;
+      const float old = exp2_hw(fmaf(ref[u], c2, -tc));
+      ref[u] = top;
+      sum[u] *= old;
+      x[u] *= old;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const float a = i0 + i < n ? exp2_hw(fmaf(y[u][i].x, c2, -tc)) : 0.f;
+        sum[u] = fmaf(y[u][i].y, a, sum[u]);
+        x[u] = f32x4_t{fmaf(z0[u][i].x, a, x[u][0]), fmaf(z0[u][i].y, a, x[u][1]), fmaf(z1[u][i].x, a, x[u][2]),
+                       fmaf(z1[u][i].y, a, x[u][3])};
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = (u * NW + wave) * kPer + lane / kL;
+    if (r < n_out) put(r, d, x[u], ref[u], sum[u]);
+  }
+}
+template <int D, typename Put>
+__device__ __forceinline__ void join(const DecodeArgs& p, float c2, int n_out, int at, int n, int step, Put&& put) {
+  constexpr int kPer = 256 / D * NW;                   // rows the workgroup takes at once
+  if (n_out <= kPer) join_units<D, 1, 16>(p, c2, n_out, at, n, step, put);
+  else join_units<D, kRows / kPer, 4 * kPer / 8>(p, c2, n_out, at, n, step, put);
+}
+
 template <int D>
 constexpr int join_row() { return D + 4; }             // floats; padded against bank conflicts
 template <int D>
@@ -160,7 +273,7 @@ void decode_kernel(DecodeArgs p) {
   __shared__ __attribute__((aligned(16))) float smem[smem_bytes<D>() / 4];
   const int lane = threadIdx.x & 63, g = lane >> 5, r32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Seg sg = find_work(p, blockIdx.x, true);
+  const Seg sg = find_work(p, runs_of_8(blockIdx.x, gridDim.x));
   if (sg.b < 0) return;
   const int rt = sg.rest % sg.row_tiles;
   const int hp = sg.rest / sg.row_tiles;
@@ -333,7 +446,7 @@ void decode_kernel(DecodeArgs p) {
   }
   l += other_half(l);
 
-  // the four waves' sums, brought to the largest reference, added in order
+  // the waves' sums, brought to the largest reference, added in order
   constexpr int kJ = join_row<D>();
   float2* ml = reinterpret_cast<float2*>(smem + NW * kRows * kJ);
   if (g == 0) ml[wave * kRows + r32] = make_float2(m, l);
@@ -362,6 +475,16 @@ void decode_kernel(DecodeArgs p) {
   if (wave == 0 && g == 0) ml[r32] = make_float2(top, all);
   lds_barrier();
   const int n_out = min(kRows, n_rows - rt * kRows);
+  auto store = [&](int r, int d, f32x4_t x, float ref, float sum) {
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    const int t = quot(rt * kRows + r, p.g), hh = head * p.g.d + rt * kRows + r - t * p.g.d;
+    const int64_t at = static_cast<int64_t>(sg.start) + t;
+    *reinterpret_cast<uint2*>(p.out + at * p.out_ld + hh * D + d) =
+        pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    if (p.lse && d == 0) p.lse[at * p.nh + hh] = sum == 0.f ? -INFINITY : fmaf(ref, p.scale, log2_hw(sum) * kLn2);
+  };
+  // the segment's pieces are `step` places apart
+  const int step = p.nkv * sg.row_tiles, first = sg.part + head * sg.row_tiles + rt;
   for (int i = threadIdx.x; i < n_out * (D / 4); i += 64 * NW) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     f32x4_t x = *reinterpret_cast<const f32x4_t*>(smem + r * kJ + d);
@@ -369,77 +492,38 @@ void decode_kernel(DecodeArgs p) {
     for (int w = 1; w < NW; ++w) x += *reinterpret_cast<const f32x4_t*>(smem + (w * kRows + r) * kJ + d);
     const float2 y = ml[r];
     if (sg.pieces == 1) {
-      const float inv = y.y > 0.f ? 1.f / y.y : (y.y == 0.f ? 0.f : y.y);
-      const int t = quot(rt * kRows + r, p.g), hh = head * p.g.d + rt * kRows + r - t * p.g.d;
-      const int64_t at = static_cast<int64_t>(sg.start) + t;
-      *reinterpret_cast<uint2*>(p.out + at * p.out_ld + hh * D + d) =
-          pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-      if (p.lse && d == 0)
-        p.lse[at * p.nh + hh] = y.y == 0.f ? -INFINITY : fmaf(y.x, p.scale, log2_hw(y.y) * kLn2);
+      store(r, d, x, y.x, y.y);
     } else {
-      const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + r;
-      *reinterpret_cast<f32x4_t*>(p.part + at * D + d) = x;
-      if (d == 0) p.part_ml[at] = y;
+      const int64_t at = static_cast<int64_t>(first + piece * step) * kRows + r;
+      put2(p.part + at * D + d, x[0], x[1]);
+      put2(p.part + at * D + d + 2, x[2], x[3]);
+      if (d == 0) put2(p.part_ml + at, y.x, y.y);
     }
   }
-}
+  if (sg.pieces == 1) return;
 
-// ---- joining the pieces ------------------------------------------------------------
-// A workgroup takes 256 / D of a segment's rows (2 or 4), its waves the pieces
-// in turn; D / 4 lanes a row.
-template <int D>
-__global__ __launch_bounds__(256) void join_kernel(DecodeArgs p) {
-  constexpr int kL = D / 4, kPer = 64 / kL, kSlots = kRows / kPer;
-  __shared__ __attribute__((aligned(16))) float red[4][64][5];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Seg sg = find_work(p, blockIdx.x / kSlots, false);
-  if (sg.b < 0 || sg.pieces == 1) return;
-  // with offsets that overlap the work can exceed the grid: no such piece was stored
-  if (static_cast<int64_t>(sg.first) + static_cast<int64_t>(p.nkv) * sg.row_tiles * sg.pieces > p.wgs) return;
-  const int rt = sg.rest % sg.row_tiles, head = sg.rest / sg.row_tiles;
-  const int n_out = min(kRows, sg.n_q * p.g.d - rt * kRows);
-  const int r_first = (blockIdx.x % kSlots) * kPer;
-  if (r_first >= n_out) return;
-  const int r = r_first + lane / kL, d = (lane % kL) * 4;
-  const int rc = min(r, n_out - 1);
-  const int64_t step = static_cast<int64_t>(p.nkv) * sg.row_tiles * kRows;
-  const int64_t at = (static_cast<int64_t>(sg.first) + head * sg.row_tiles + rt) * kRows + rc;
-  const float c2 = p.scale * kLog2e;
-  // largest reference of the row: the lanes of the row share the pieces
-  float top = -INFINITY;
-  for (int i = lane % kL; i < sg.pieces; i += kL) top = fmaxf(top, p.part_ml[at + i * step].x);
-#pragma unroll
-  for (int o = kL / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  const float tc = top == -INFINITY ? 0.f : top * c2;
-  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = wave; i < sg.pieces; i += 4) {
-    const float2 y = p.part_ml[at + i * step];
-    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(p.part + (at + i * step) * D + d);
-    const float a = exp2_hw(fmaf(y.x, c2, -tc));
-    l = fmaf(y.y, a, l);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] = fmaf(x[j], a, sum[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) red[wave][lane][j] = sum[j];
-  red[wave][lane][4] = l;
-  __syncthreads();
-  if (wave == 0 && r < n_out) {
-#pragma unroll
-    for (int w = 1; w < 4; ++w) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += red[w][lane][j];
-      l += red[w][lane][4];
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int t = quot(rt * kRows + r, p.g), hh = head * p.g.d + rt * kRows + r - t * p.g.d;
-    const int64_t o = static_cast<int64_t>(sg.start) + t;
-    *reinterpret_cast<uint2*>(p.out + o * p.out_ld + hh * D + d) =
-        pack4(sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
-    if (p.lse && d == 0) p.lse[o * p.nh + hh] = l == 0.f ? -INFINITY : fmaf(top, p.scale, log2_hw(l) * kLn2);
-  }
+  // The last piece of a group of kJoin joins them, the last group of the
+  // segment the groups.
+  int* flag = reinterpret_cast<int*>(smem);
+  if (!last_of(p.done + first + piece / kJoin * kJoin * step, min(kJoin, sg.pieces - piece / kJoin * kJoin), flag))
+    return;
+  const bool one = sg.pieces <= kJoin;
+  const int g0 = first + piece / kJoin * kJoin * step;
+  auto keep = [&](int r, int d, f32x4_t x, float ref, float sum) {
+    const int64_t at = static_cast<int64_t>(g0) * kRows + r;
+    put2(p.part + at * D + d, x[0], x[1]);
+    put2(p.part + at * D + d + 2, x[2], x[3]);
+    if (d == 0) put2(p.part_ml + at, ref, sum);
+  };
+  auto both = [&](int r, int d, f32x4_t x, float ref, float sum) {
+    if (one) store(r, d, x, ref, sum);
+    else keep(r, d, x, ref, sum);
+  };
+  join<D>(p, c2, n_out, g0, min(kJoin, sg.pieces - piece / kJoin * kJoin), step, both);
+  if (one) return;
+  const int groups = (sg.pieces + kJoin - 1) / kJoin;
+  if (!last_of(p.done + kParts + first, groups, flag)) return;
+  join<D>(p, c2, n_out, first, groups, step * kJoin, store);
 }
 
 // (request, head, 32 rows) of a call: B requests share T tokens
@@ -449,22 +533,16 @@ int64_t segments(int B, int T, int nh, int nkv) {
 
 template <int D>
 void launch_decode(const DecodeArgs& a, hipStream_t stream) {
-  const int64_t segs = segments(a.B, a.T, a.nh, a.nkv);
-  hipLaunchKernelGGL(decode_kernel<D>, dim3(static_cast<unsigned>(segs + kPieces)), dim3(64 * NW), 0, stream, a);
-  constexpr int kSlots = kRows / (64 / (D / 4));
-  hipLaunchKernelGGL(join_kernel<D>, dim3(static_cast<unsigned>(segs * kSlots)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(decode_kernel<D>, dim3(static_cast<unsigned>(a.segs + kPieces)), dim3(64 * NW), 0, stream, a);
 }
 
 }  // namespace
 }  // namespace gqa
 }  // namespace moe
 
-extern "C" size_t moe_gqa_decode_workspace(int B, int T, int n_heads, int n_kv_heads, int head_dim) {
-  if (B < 1 || B > 65536 || T < 1 || n_heads < 1 || n_heads > 1024 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 ||
-      (head_dim != 64 && head_dim != 128) || static_cast<int64_t>(T) * n_heads > (1 << 24))
-    return 0;
-  const size_t wgs = static_cast<size_t>(moe::gqa::segments(B, T, n_heads, n_kv_heads)) + moe::gqa::kPieces;
-  return wgs * moe::gqa::kRows * (static_cast<size_t>(head_dim) * 4 + 8);
+extern "C" size_t moe_gqa_decode_workspace(int head_dim) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return moe::gqa::kParts * 8 + static_cast<size_t>(moe::gqa::kParts) * moe::gqa::kRows * (head_dim * 4 + 8);
 }
 
 extern "C" int moe_gqa_decode(const void* q, int64_t q_ld, int fmt, const void* k_cache, const void* v_cache,
@@ -490,8 +568,8 @@ extern "C" int moe_gqa_decode(const void* q, int64_t q_ld, int fmt, const void* 
               MOE_ERR_INVALID_ARG, "moe_gqa_decode: null pointer");
   MOE_REQUIRE(aligned16(q) && aligned16(k_cache) && aligned16(v_cache) && aligned16(out) && aligned16(ws),
               MOE_ERR_ALIGNMENT, "moe_gqa_decode: q, the cache, out and ws must be 16-byte aligned");
-  MOE_REQUIRE(ws && ws_bytes >= moe_gqa_decode_workspace(B, T, n_heads, n_kv_heads, head_dim), MOE_ERR_WORKSPACE,
-              "moe_gqa_decode: ws smaller than moe_gqa_decode_workspace(...)");
+  MOE_REQUIRE(ws && ws_bytes >= moe_gqa_decode_workspace(head_dim), MOE_ERR_WORKSPACE,
+              "moe_gqa_decode: ws smaller than moe_gqa_decode_workspace(head_dim)");
   DecodeArgs a{};
   a.q = static_cast<const uint16_t*>(q), a.q_ld = q_ld;
   a.k = static_cast<const uint8_t*>(k_cache), a.v = static_cast<const uint8_t*>(v_cache);
@@ -501,10 +579,10 @@ extern "C" int moe_gqa_decode(const void* q, int64_t q_ld, int fmt, const void* 
   a.tree = reinterpret_cast<const uint64_t*>(tree_mask);
   a.B = B, a.T = T, a.nh = n_heads, a.nkv = n_kv_heads, a.g = make_div(n_heads / n_kv_heads), a.scale = scale;
   a.out = static_cast<uint16_t*>(out), a.out_ld = out_ld, a.lse = lse;
-  const size_t wgs = static_cast<size_t>(segments(B, T, n_heads, n_kv_heads)) + kPieces;
-  a.wgs = static_cast<int>(wgs);
-  a.part = static_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(a.part + wgs * kRows * head_dim);
+  a.segs = static_cast<int>(segments(B, T, n_heads, n_kv_heads));
+  a.done = static_cast<int*>(ws);
+  a.part = reinterpret_cast<float*>(a.done + 2 * kParts);
+  a.part_ml = reinterpret_cast<float2*>(a.part + static_cast<size_t>(kParts) * kRows * head_dim);
   if (head_dim == 128) launch_decode<128>(a, stream);
   else launch_decode<64>(a, stream);
   return check_launch(fn);

@@ -23,6 +23,7 @@ from . import _lib as L
 
 BLOCK = 16                 # cached tokens that share a scale
 DIMS = (64, 128)
+_BF, _I32 = torch.bfloat16, torch.int32
 
 
 def _heads(n_heads, n_kv_heads, head_dim):
@@ -32,31 +33,38 @@ def _heads(n_heads, n_kv_heads, head_dim):
         raise ValueError(f"n_heads must be a multiple of n_kv_heads and at most 1024, got {n_heads}, {n_kv_heads}")
 
 
-def _here(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+# the checks below run on every call, beside kernels of a few microseconds: they
+# ask for plain numbers (torch's device objects and shape slices cost a third
+# of a microsecond each)
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(t: torch.Tensor, name: str) -> int:
+    """The current device's number, which has to be t's."""
+    dev = t.get_device()
+    if dev < 0 or dev != _current():
         raise ValueError(f"{name} must be on the current GPU, got {t.device}")
+    return dev
 
 
-def _rows(t: torch.Tensor, name: str, heads: int, dim: int) -> int:
-    """Row stride of a bf16 tensor [tokens, heads, dim] whose tokens are dense
-    inside (the tensor may be a slice of wider rows)."""
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be a bfloat16 tensor, got {t.dtype}")
-    shape, stride = t.shape, t.stride()
-    if shape[1:] != (heads, dim):
-        raise ValueError(f"{name} must have shape [tokens, {heads}, {dim}], got {tuple(shape)}")
-    _here(t, name)
-    if shape[0] > 0 and (stride[2] != 1 or (stride[1] != dim and heads > 1)):
+def _rows(t: torch.Tensor, name: str, heads: int, dim: int, dev: int) -> int:
+    """Row stride of a bf16 tensor [tokens, heads, dim] on device dev whose
+    tokens are dense inside (the tensor may be a slice of wider rows)."""
+    shape = t.shape
+    if t.dtype is not _BF or len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor [tokens, {heads}, {dim}] on the current GPU, got {t.dtype} "
+                         f"{tuple(shape)} on {t.device}")
+    row, head, one = t.stride()
+    if shape[0] > 0 and (one != 1 or (head != dim and heads > 1)):
         raise ValueError(f"{name}: a token's values must be consecutive")
     # a lone token's stride is never used, and may be anything
-    return stride[0] if shape[0] > 1 else heads * dim
+    return row if shape[0] > 1 else heads * dim
 
 
-def _vec(t: torch.Tensor, name: str, dtype, shape: tuple) -> torch.Tensor:
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape}, got {t.dtype} {tuple(t.shape)}")
-    _here(t, name)
-    return t
+def _vec(t: torch.Tensor, name: str, dtype, shape: tuple, dev: int) -> None:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on the current GPU, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
 
 
 def _first(t: torch.Tensor, n: int) -> torch.Tensor:
@@ -90,29 +98,32 @@ class QKNormRope:
         T, h, kv, d = q.shape[0], self.n_heads, self.n_kv_heads, self.head_dim
         if T > self.T or k.shape[0] != T:
             raise ValueError(f"at most {self.T} tokens, as many rows of k as of q")
-        for w, name in ((w_q, "w_q"), (w_k, "w_k")):
-            if w is not None:
-                _vec(w, name, torch.bfloat16, (d,))
+        dev = _here(q, "q")
+        if w_q is not None:
+            _vec(w_q, "w_q", _BF, (d,), dev)
+        if w_k is not None:
+            _vec(w_k, "w_k", _BF, (d,), dev)
         if (cos is None) != (sin is None):
             raise ValueError("cos and sin come together")
         max_pos = 1
         if cos is not None:
             max_pos = cos.shape[0]
-            _vec(cos, "cos", torch.float32, (max_pos, self.rotary // 2))
-            _vec(sin, "sin", torch.float32, (max_pos, self.rotary // 2))
+            table = (max_pos, self.rotary // 2)
+            _vec(cos, "cos", torch.float32, table, dev)
+            _vec(sin, "sin", torch.float32, table, dev)
             if positions is None:
                 raise ValueError("a rotation needs positions")
-            _vec(positions, "positions", torch.int32, (T,))
-        head = (q, _rows(q, "q", h, d), k, _rows(k, "k", kv, d), L.MOE_BF16, w_q, w_k, self.eps, cos, sin, max_pos,
-                positions, self.rotary, self.interleaved, T, h, kv, d)
-        return head, T
+            _vec(positions, "positions", _I32, (T,), dev)
+        head = (q, _rows(q, "q", h, d, dev), k, _rows(k, "k", kv, d, dev), L.MOE_BF16, w_q, w_k, self.eps, cos, sin,
+                max_pos, positions, self.rotary, self.interleaved, T, h, kv, d)
+        return head, T, dev
 
     def forward(self, q, k, w_q=None, w_k=None, cos=None, sin=None, positions=None, stream=None):
         """q [T, n_heads, head_dim] and k [T, n_kv_heads, head_dim] bf16 (may be
         slices of a projection's rows), w_q and w_k [head_dim] bf16 (without one:
         not normalized), cos and sin [max_pos, rotary / 2] fp32, positions [T]
         int32. Returns the new q and k."""
-        head, T = self._inputs(q, k, w_q, w_k, cos, sin, positions)
+        head, T, _ = self._inputs(q, k, w_q, w_k, cos, sin, positions)
         d = self.head_dim
         L.moe_qk_norm_rope(*head, self.q, self.n_heads * d, self.k, self.n_kv_heads * d, stream)
         return _first(self.q, T), _first(self.k, T)
@@ -125,12 +136,13 @@ class QKNormRope:
         for a side without weight."""
         if not self.has_backward:
             raise ValueError("built without backward=True")
-        head, T = self._inputs(q, k, w_q, w_k, cos, sin, positions)
+        head, T, dev = self._inputs(q, k, w_q, w_k, cos, sin, positions)
         h, kv, d = self.n_heads, self.n_kv_heads, self.head_dim
         if dq_out.shape[0] != T or dk_out.shape[0] != T:
             raise ValueError(f"expected {T} rows of dq_out and dk_out")
-        L.moe_qk_norm_rope_bwd(dq_out, _rows(dq_out, "dq_out", h, d), dk_out, _rows(dk_out, "dk_out", kv, d), *head,
-                               self.dq, h * d, self.dk, kv * d, self.dw_q, self.dw_k, self.ws, stream)
+        L.moe_qk_norm_rope_bwd(dq_out, _rows(dq_out, "dq_out", h, d, dev), dk_out,
+                               _rows(dk_out, "dk_out", kv, d, dev), *head, self.dq, h * d, self.dk, kv * d, self.dw_q,
+                               self.dw_k, self.ws, stream)
         return (_first(self.dq, T), _first(self.dk, T), None if w_q is None else self.dw_q,
                 None if w_k is None else self.dw_k)
 
@@ -167,14 +179,16 @@ class GroupedAttention:
             raise ValueError(f"at most {self.Tq} queries and {self.Tk} keys, as many rows of v as of k")
         if not 0 <= B <= self.n_seqs:
             raise ValueError(f"cu_q must describe at most {self.n_seqs} sequences")
-        _vec(cu_q, "cu_q", torch.int32, (B + 1,))
-        _vec(cu_k, "cu_k", torch.int32, (B + 1,))
-        return (q, _rows(q, "q", h, d), k, _rows(k, "k", kv, d), v, _rows(v, "v", kv, d), L.MOE_BF16), B, Tq, Tk
+        dev = _here(q, "q")
+        _vec(cu_q, "cu_q", _I32, (B + 1,), dev)
+        _vec(cu_k, "cu_k", _I32, (B + 1,), dev)
+        return (q, _rows(q, "q", h, d, dev), k, _rows(k, "k", kv, d, dev), v, _rows(v, "v", kv, d, dev),
+                L.MOE_BF16), B, Tq, Tk, dev
 
     def forward(self, q, k, v, cu_q, cu_k, stream=None):
         """out [q's rows, n_heads, head_dim] bf16 and lse [q's rows, n_heads]
         fp32; k and v [Tk, n_kv_heads, head_dim]."""
-        ins, B, Tq, Tk = self._inputs(q, k, v, cu_q, cu_k)
+        ins, B, Tq, Tk, _ = self._inputs(q, k, v, cu_q, cu_k)
         h, d = self.n_heads, self.head_dim
         L.moe_gqa_attn_fwd(*ins, cu_q, cu_k, B, Tq, Tk, h, self.n_kv_heads, d, self.causal, self.scale, self.out,
                            h * d, self.lse, stream)
@@ -186,13 +200,13 @@ class GroupedAttention:
         """Gradients (dq, dk, dv) of the last forward, on its inputs."""
         if not self.has_backward:
             raise ValueError("built without backward=True")
-        ins, B, Tq, Tk = self._inputs(q, k, v, cu_q, cu_k)
+        ins, B, Tq, Tk, dev = self._inputs(q, k, v, cu_q, cu_k)
         h, kv, d = self.n_heads, self.n_kv_heads, self.head_dim
         if dout.shape[0] != Tq:
             raise ValueError(f"expected {Tq} rows of dout")
-        L.moe_gqa_attn_bwd(dout, _rows(dout, "dout", h, d), *ins, self.out, h * d, self.lse, cu_q, cu_k, B, Tq, Tk, h,
-                           kv, d, self.causal, self.scale, self.dq, h * d, self.dk, kv * d, self.dv, kv * d, self.ws,
-                           stream)
+        L.moe_gqa_attn_bwd(dout, _rows(dout, "dout", h, d, dev), *ins, self.out, h * d, self.lse, cu_q, cu_k, B, Tq,
+                           Tk, h, kv, d, self.causal, self.scale, self.dq, h * d, self.dk, kv * d, self.dv, kv * d,
+                           self.ws, stream)
         return _first(self.dq, Tq), _first(self.dk, Tk), _first(self.dv, Tk)
 
 
@@ -211,11 +225,12 @@ class GroupedCache:
                              f"got {tuple(k.shape)}")
         self.n_pages, self.n_kv_heads, blocks = k.shape[:3]
         self.head_dim, self.page_size = k.shape[3] * 16, blocks * BLOCK
-        head = (self.n_pages, self.n_kv_heads, blocks)
-        self.k = _vec(k, "k", torch.uint8, tuple(k.shape))
-        self.v = _vec(v, "v", torch.uint8, (*head, self.head_dim // 2, 2, 2, 2, 4))
-        self.k_scales = _vec(k_scales, "k_scales", torch.uint8, head)
-        self.v_scales = _vec(v_scales, "v_scales", torch.uint8, head)
+        self.device, u8, head = _here(k, "k"), torch.uint8, (self.n_pages, self.n_kv_heads, blocks)
+        _vec(k, "k", u8, tuple(k.shape), self.device)
+        _vec(v, "v", u8, (*head, self.head_dim // 2, 2, 2, 2, 4), self.device)
+        _vec(k_scales, "k_scales", u8, head, self.device)
+        _vec(v_scales, "v_scales", u8, head, self.device)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
 
     @classmethod
     def empty(cls, n_pages, page_size, n_kv_heads, head_dim=128, device="cuda"):
@@ -233,11 +248,13 @@ class GroupedCache:
         return self.k, self.v, self.k_scales, self.v_scales, self.page_size, self.n_pages
 
 
-def _requests(page_table, lens, cu):
+def _requests(cache, page_table, lens, cu, dev):
     B = lens.shape[0]
-    _vec(page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
-    _vec(lens, "lens", torch.int32, (B,))
-    _vec(cu, "cu", torch.int32, (B + 1,))
+    if cache.device != dev:
+        raise ValueError(f"the cache must be on the current GPU, got cuda:{cache.device}")
+    _vec(page_table, "page_table", _I32, (B, page_table.shape[-1]), dev)
+    _vec(lens, "lens", _I32, (B,), dev)
+    _vec(cu, "cu", _I32, (B + 1,), dev)
     return B
 
 
@@ -249,10 +266,10 @@ def grouped_cache_append(k, v, cache, page_table, lens, cu, stream=None):
     T, kv, d = k.shape[0], cache.n_kv_heads, cache.head_dim
     if v.shape[0] != T:
         raise ValueError("as many rows of v as of k")
-    B = _requests(page_table, lens, cu)
-    _here(cache.k, "cache")
-    L.moe_gqa_append(k, _rows(k, "k", kv, d), v, _rows(v, "v", kv, d), L.MOE_BF16, *cache._tensors(), page_table,
-                     page_table.shape[1], lens, cu, B, T, kv, d, stream)
+    dev = _here(k, "k")
+    B = _requests(cache, page_table, lens, cu, dev)
+    L.moe_gqa_append(k, _rows(k, "k", kv, d, dev), v, _rows(v, "v", kv, d, dev), L.MOE_BF16, *cache._tensors(),
+                     page_table, page_table.shape[1], lens, cu, B, T, kv, d, stream)
 
 
 class GroupedDecode:
@@ -261,14 +278,17 @@ class GroupedDecode:
 
     def __init__(self, *, n_heads, n_kv_heads, head_dim=128, max_tokens, max_seqs, scale=None, device="cuda"):
         _heads(n_heads, n_kv_heads, head_dim)
+        if not (1 <= max_seqs <= 65536 and max_seqs * n_kv_heads <= 1 << 19 and 1 <= max_tokens and
+                max_tokens * n_heads <= 1 << 24):
+            raise ValueError("moe_gqa_decode does not support these sizes")
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
         self.max_tokens, self.max_seqs = max_tokens, max_seqs
         self.scale = head_dim ** -0.5 if scale is None else scale
         self.out = torch.empty((max_tokens, n_heads, head_dim), dtype=torch.bfloat16, device=device)
-        nws = L.moe_gqa_decode_workspace(max_seqs, max_tokens, n_heads, n_kv_heads, head_dim)
-        if nws == 0:
-            raise ValueError("moe_gqa_decode does not support these sizes")
-        self.ws = torch.empty((nws,), dtype=torch.uint8, device=device)
+        # zeros once: where a call counts the pieces of its work, and leaves zeros
+        self.ws = torch.zeros((L.moe_gqa_decode_workspace(head_dim),), dtype=torch.uint8, device=device)
+        if self.ws.is_cuda:                # the first call may be on another stream
+            torch.cuda.current_stream(self.ws.device).synchronize()
 
     def __call__(self, q, cache, page_table, lens, cu_q, tree_mask=None, lse=None, stream=None):
         """q [T, n_heads, head_dim] bf16 (normalized and rotated), the new
@@ -277,16 +297,16 @@ class GroupedDecode:
         tree_mask optional [T] int64, lse optional [T, n_heads] fp32 (filled).
         Returns out [T, n_heads, head_dim], a view of the object's buffer."""
         T, h, kv, d = q.shape[0], self.n_heads, self.n_kv_heads, self.head_dim
-        B = _requests(page_table, lens, cu_q)
+        dev = _here(q, "q")
+        B = _requests(cache, page_table, lens, cu_q, dev)
         if T > self.max_tokens or B > self.max_seqs:
             raise ValueError(f"at most {self.max_tokens} tokens of {self.max_seqs} requests")
         if (cache.n_kv_heads, cache.head_dim) != (kv, d):
             raise ValueError(f"the cache holds {cache.n_kv_heads} heads of {cache.head_dim}, expected {kv} of {d}")
-        _here(cache.k, "cache")
         if tree_mask is not None:
-            _vec(tree_mask, "tree_mask", torch.int64, (T,))
+            _vec(tree_mask, "tree_mask", torch.int64, (T,), dev)
         if lse is not None:
-            _vec(lse, "lse", torch.float32, (T, h))
-        L.moe_gqa_decode(q, _rows(q, "q", h, d), L.MOE_BF16, *cache._tensors(), page_table, page_table.shape[1], lens,
+            _vec(lse, "lse", torch.float32, (T, h), dev)
+        L.moe_gqa_decode(q, _rows(q, "q", h, d, dev), L.MOE_BF16, *cache._tensors(), page_table, page_table.shape[1], lens,
                          cu_q, tree_mask, B, T, h, kv, d, self.scale, self.out, h * d, lse, self.ws, stream)
         return _first(self.out, T)

@@ -145,12 +145,9 @@ def test_decode_refusals(lib):
         assert _dec(lib, **bad) == INVALID, bad
     for bad in (dict(q=A + 8), dict(out=A + 8), dict(ws=A + 8), dict(q_ld=260)):
         assert _dec(lib, **bad) == ALIGN, bad
-    need = lib.moe_gqa_decode_workspace(1, 4, 2, 1, 128)
+    need = lib.moe_gqa_decode_workspace(128)
     assert _dec(lib, wsb=need - 1) == WS and _dec(lib, ws=None) == WS
-    for bad in ((0, 4, 2, 1, 128), (1, 0, 2, 1, 128), (1, 4, 3, 2, 128), (1, 4, 2, 1, 96), (1, 1 << 24, 2, 1, 128)):
-        assert lib.moe_gqa_decode_workspace(*bad) == 0
-    sizes = [[lib.moe_gqa_decode_workspace(b, t, 12, 2, 64) for t in range(1, 90)] for b in range(1, 70)]
-    assert all(row == sorted(row) for row in sizes) and all(list(c) == sorted(c) for c in zip(*sizes))
+    assert lib.moe_gqa_decode_workspace(96) == 0 and 0 < lib.moe_gqa_decode_workspace(64) < need
 
 
 # ---- the classes, with tensors in host memory: none may reach a kernel ----------
@@ -205,24 +202,22 @@ def test_classes_refuse_sizes():
 def test_rows_of_no_tokens_and_of_one():
     """Strides that are never used may be anything; a token's values may not."""
     class T:
-        dtype, is_cuda = BF, True
-        device = torch.device("cuda", 0)
-        shape, st = torch.Size((0, 3, 64)), (0, 0, 0)
+        dtype, device, shape, st = BF, "cuda:0", torch.Size((0, 3, 64)), (0, 0, 0)
 
         def stride(self):
             return self.st
 
-    t, cur = T(), torch.cuda.current_device
-    torch.cuda.current_device = lambda: 0
-    try:
-        assert gqa._rows(t, "q", 3, 64) == 192
-        t.shape, t.st = torch.Size((1, 3, 64)), (7, 64, 1)
-        assert gqa._rows(t, "q", 3, 64) == 192
-        t.st = (7, 128, 1)
-        with pytest.raises(ValueError, match="consecutive"):
-            gqa._rows(t, "q", 3, 64)
-        T.device = torch.device("cuda", 1)
-        with pytest.raises(ValueError, match="current GPU"):
-            gqa._rows(t, "q", 3, 64)
-    finally:
-        torch.cuda.current_device = cur
+        def get_device(self):
+            return 0
+
+    t = T()
+    assert gqa._rows(t, "q", 3, 64, 0) == 192
+    t.shape, t.st = torch.Size((1, 3, 64)), (7, 64, 1)
+    assert gqa._rows(t, "q", 3, 64, 0) == 192
+    t.st = (7, 128, 1)
+    with pytest.raises(ValueError, match="consecutive"):
+        gqa._rows(t, "q", 3, 64, 0)
+    with pytest.raises(ValueError, match="current GPU"):
+        gqa._rows(t, "q", 3, 64, 1)
+    with pytest.raises(ValueError, match="current GPU"):
+        gqa._here(torch.zeros(1), "q")
