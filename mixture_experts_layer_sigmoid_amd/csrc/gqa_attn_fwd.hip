@@ -115,11 +115,10 @@ void attn_fwd_kernel(FwdArgs p) {
     if (t0 > wave_last) continue;          // nothing of this tile is visible to the wave
     f32x16_t s[2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      s[b] = f32x16_t{};
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) s[b] = mfma(row_operand(buf, k_off[k] + b * 32 * RB), qf[k], s[b]);
-    }
+      for (int k = 0; k < D / 16; ++k)
+        s[b] = mfma(row_operand(buf, k_off[k] + b * 32 * RB), qf[k], k == 0 ? f32x16_t{} : s[b]);
     if (t0 + kKt - 1 > wave_first) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
