@@ -63,17 +63,18 @@ __device__ __forceinline__ u32x4_t pack8(const float* v) {
 
 // What a lane keeps for one token: its two pieces' places in a head, and the
 // 8 angles of their pairs where they are rotated.
-template <int D>
+// IL: pairs are neighbours. (One kernel for both orders would keep both
+// results of every rotation: 173 registers a lane of the backward.)
+template <int D, bool IL>
 struct Lane {
   int a, b;                 // first values of the two pieces
-  bool turn, halves;
+  bool turn;
   float c[8], s[8];
   __device__ __forceinline__ Lane(const NormArgs& p, int lane) {
     const int j = lane & (D / 16 - 1);
     turn = j < p.rotary / 16;
-    halves = turn && !p.interleaved;
-    a = halves ? 8 * j : 16 * j;
-    b = halves ? 8 * j + p.rotary / 2 : 16 * j + 8;
+    a = turn && !IL ? 8 * j : 16 * j;
+    b = turn && !IL ? 8 * j + p.rotary / 2 : 16 * j + 8;
   }
   __device__ __forceinline__ void angles(const NormArgs& p, int t, int lane) {
     if (!turn) return;
@@ -93,20 +94,12 @@ struct Lane {
   // pairs turned by their angles, forwards (sign 1) or back (-1)
   __device__ __forceinline__ void rotate(float* v, float sign) const {
     if (!turn) return;
-    if (halves) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = v[i], y = v[8 + i], sn = sign * s[i];
-        v[i] = x * c[i] - y * sn;
-        v[8 + i] = x * sn + y * c[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = v[2 * i], y = v[2 * i + 1], sn = sign * s[i];
-        v[2 * i] = x * c[i] - y * sn;
-        v[2 * i + 1] = x * sn + y * c[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      constexpr int kStep = IL ? 2 : 1, kMate = IL ? 1 : 8;
+      const float x = v[kStep * i], y = v[kStep * i + kMate], sn = sign * s[i];
+      v[kStep * i] = x * c[i] - y * sn;
+      v[kStep * i + kMate] = x * sn + y * c[i];
     }
   }
 };
@@ -127,14 +120,14 @@ __device__ __forceinline__ float inv_rms(const float* x, float eps) {
   return 1.f / sqrtf(head_sum<D>(s) / D + eps);
 }
 
-template <int D>
+template <int D, bool IL>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs p) {
   constexpr int kHeads = 64 / (D / 16);                // heads a wave takes at once
   const int lane = threadIdx.x & 63;
   const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
   const int t = wave / p.wpt;
   if (t >= p.T) return;
-  Lane<D> ln(p, lane);
+  Lane<D, IL> ln(p, lane);
   ln.angles(p, t, lane);
   const int first = (wave - t * p.wpt) * kHeads + lane / (D / 16), step = p.wpt * kHeads;
   auto side = [&](const uint16_t* x, int64_t ld, const uint16_t* w, uint16_t* out, int64_t out_ld, int n, int from) {
@@ -160,85 +153,91 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs p) {
 }
 
 // ---- backward --------------------------------------------------------------------
-// Workgroups take tokens in turn and add their share of dw up in registers;
-// part holds one row a workgroup, which a second launch adds in order.
-constexpr int kBwdGroups = 1024;
+// Workgroups take tokens in turn, the queries' heads first and then the keys',
+// and add their share of dw up in registers; part holds one row a workgroup,
+// which a second launch adds in order.
+constexpr int kBwdGroups = 512, kBwdWaves = 8;
 
-template <int D>
-__global__ __launch_bounds__(256) void norm_rope_bwd_kernel(NormArgs p) {
+template <int D, bool IL>
+__global__ __launch_bounds__(64 * kBwdWaves) void norm_rope_bwd_kernel(NormArgs p) {
   constexpr int kL = D / 16, kHeads = 64 / kL;
-  __shared__ float red[4][2][D];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  Lane<D> ln(p, lane);
-  float dw[2][16];
+  __shared__ float red[kBwdWaves][2][D];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Lane<D, IL> ln(p, lane);
+  auto side = [&](int which, const uint16_t* x0, int64_t ld, const uint16_t* w, const uint16_t* dy0, int64_t dy_ld,
+                  uint16_t* dx0, int64_t dx_ld, int n) {
+    float wv[16], dw[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dw[0][i] = dw[1][i] = 0.f;
-  auto side = [&](int t, const uint16_t* x, int64_t ld, const uint16_t* w, const uint16_t* dy, int64_t dy_ld,
-                  uint16_t* dx, int64_t dx_ld, int n, float* sum) {
-    float wv_[16];
-    if (w) ln.load(w, wv_);
-    x += t * ld;
-    dy += t * dy_ld;
-    dx += t * dx_ld;
-    for (int h = lane / kL; h < n; h += kHeads) {
-      float g[16];
-      ln.load(dy + h * D, g);
-      if (w) {
-        float v[16];
-        ln.load(x + h * D, v);
-        const float r = inv_rms<D>(v, p.eps);
-        ln.rotate(g, -1.f);
-        float dot = 0.f;
+    for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+    if (w) ln.load(w, wv);
+    for (int t = blockIdx.x * kBwdWaves + wave; t < p.T; t += gridDim.x * kBwdWaves) {
+      ln.angles(p, t, lane);
+      const uint16_t* x = x0 + t * ld;
+      const uint16_t* dy = dy0 + t * dy_ld;
+      uint16_t* dx = dx0 + t * dx_ld;
+      for (int h = lane / kL; h < n; h += kHeads) {
+        float g[16];
+        ln.load(dy + h * D, g);
+        if (w) {
+          float v[16];
+          ln.load(x + h * D, v);
+          const float r = inv_rms<D>(v, p.eps);
+          ln.rotate(g, -1.f);
+          float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[i] *= r;
-          sum[i] = fmaf(g[i], v[i], sum[i]);
-          g[i] *= wv_[i];
-          dot = fmaf(g[i], v[i], dot);
+          for (int i = 0; i < 16; ++i) {
+            v[i] *= r;
+            dw[i] = fmaf(g[i], v[i], dw[i]);
+            g[i] *= wv[i];
+            dot = fmaf(g[i], v[i], dot);
+          }
+          dot = head_sum<D>(dot) / D;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) g[i] = r * (g[i] - v[i] * dot);
+        } else {
+          ln.rotate(g, -1.f);
         }
-        dot = head_sum<D>(dot) / D;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = r * (g[i] - v[i] * dot);
-      } else {
-        ln.rotate(g, -1.f);
+        ln.store(dx + h * D, g);
       }
-      ln.store(dx + h * D, g);
     }
-  };
-  for (int t = blockIdx.x * 4 + wv; t < p.T; t += gridDim.x * 4) {
-    ln.angles(p, t, lane);
-    side(t, p.q, p.q_ld, p.w_q, p.dq_out, p.dqo_ld, p.q_out, p.qo_ld, p.nh, dw[0]);
-    side(t, p.k, p.k_ld, p.w_k, p.dk_out, p.dko_ld, p.k_out, p.ko_ld, p.nkv, dw[1]);
-  }
-  if (!p.w_q && !p.w_k) return;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
 #pragma unroll
-      for (int o = kL; o < 64; o <<= 1) dw[s][i] += __shfl_xor(dw[s][i], o, 64);
-      if (lane < kL) red[wv][s][(i < 8 ? ln.a + i : ln.b + i - 8)] = dw[s][i];
+      for (int o = kL; o < 64; o <<= 1) dw[i] += __shfl_xor(dw[i], o, 64);
+      if (lane < kL) red[wave][which][i < 8 ? ln.a + i : ln.b + i - 8] = dw[i];
     }
+  };
+  side(0, p.q, p.q_ld, p.w_q, p.dq_out, p.dqo_ld, p.q_out, p.qo_ld, p.nh);
+  side(1, p.k, p.k_ld, p.w_k, p.dk_out, p.dko_ld, p.k_out, p.ko_ld, p.nkv);
+  if (!p.w_q && !p.w_k) return;
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += 256) {
-    const float* r = &red[0][0][0] + i;
-    p.part[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = (r[0] + r[2 * D]) + (r[4 * D] + r[6 * D]);
+  if (threadIdx.x < 2 * D) {
+    const float* r = &red[0][0][0] + threadIdx.x;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBwdWaves; ++i) s += r[i * 2 * D];
+    p.part[static_cast<int64_t>(blockIdx.x) * 2 * D + threadIdx.x] = s;
   }
 }
 
-// 16 columns a workgroup, 16 rows of part at a time
+// 16 columns a workgroup, 64 rows of part at a time
 template <int D>
-__global__ __launch_bounds__(256) void norm_rope_dw_kernel(NormArgs p) {
-  __shared__ float red[16][17];
+__global__ __launch_bounds__(1024) void norm_rope_dw_kernel(NormArgs p) {
+  __shared__ float red[64][17];
   const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
   const int col = blockIdx.x * 16 + c;
   float s = 0.f;
-#pragma unroll 8
-  for (int i = r; i < p.n_parts; i += 16) s += p.part[static_cast<int64_t>(i) * 2 * D + col];
+#pragma unroll
+  for (int i = 0; i < kBwdGroups / 64; ++i) {
+    const int row = r + 64 * i;
+    s += row < p.n_parts ? p.part[static_cast<int64_t>(row) * 2 * D + col] : 0.f;
+  }
   red[r][c] = s;
   __syncthreads();
   if (r == 0) {
-    for (int i = 1; i < 16; ++i) s += red[i][c];
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) s += red[i][c];
     float* out = col < D ? (p.w_q ? p.dw_q + col : nullptr) : (p.w_k ? p.dw_k + col - D : nullptr);
     if (out) *out = s;
   }
@@ -301,8 +300,9 @@ extern "C" int moe_qk_norm_rope(const void* q, int64_t q_ld, const void* k, int6
   a.wpt = 1;
   while (a.wpt < rounds && static_cast<int64_t>(T) * a.wpt < 8 * kNumCu) a.wpt *= 2;
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) * a.wpt + 3) / 4));
-  if (head_dim == 128) hipLaunchKernelGGL(norm_rope_kernel<128>, grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL(norm_rope_kernel<64>, grid, dim3(256), 0, stream, a);
+  const auto kernel = head_dim == 128 ? (interleaved ? norm_rope_kernel<128, true> : norm_rope_kernel<128, false>)
+                                      : (interleaved ? norm_rope_kernel<64, true> : norm_rope_kernel<64, false>);
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a);
   return check_launch(fn);
 }
 
@@ -350,14 +350,17 @@ extern "C" int moe_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ld, const vo
   a.dq_out = static_cast<const uint16_t*>(dq_out), a.dqo_ld = dqo_ld;
   a.dk_out = static_cast<const uint16_t*>(dk_out), a.dko_ld = dko_ld;
   a.dw_q = dw_q, a.dw_k = dw_k, a.part = static_cast<float*>(ws);
-  a.n_parts = (T + 3) / 4 < kBwdGroups ? (T + 3) / 4 : kBwdGroups;
+  const int groups = (T + kBwdWaves - 1) / kBwdWaves;
+  a.n_parts = groups < kBwdGroups ? groups : kBwdGroups;
   if (T > 0) {
-    if (head_dim == 128) hipLaunchKernelGGL(norm_rope_bwd_kernel<128>, dim3(a.n_parts), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(norm_rope_bwd_kernel<64>, dim3(a.n_parts), dim3(256), 0, stream, a);
+    const auto kernel = head_dim == 128
+                            ? (interleaved ? norm_rope_bwd_kernel<128, true> : norm_rope_bwd_kernel<128, false>)
+                            : (interleaved ? norm_rope_bwd_kernel<64, true> : norm_rope_bwd_kernel<64, false>);
+    hipLaunchKernelGGL(kernel, dim3(a.n_parts), dim3(64 * kBwdWaves), 0, stream, a);
   }
   if (norm) {
-    if (head_dim == 128) hipLaunchKernelGGL(norm_rope_dw_kernel<128>, dim3(16), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(norm_rope_dw_kernel<64>, dim3(8), dim3(256), 0, stream, a);
+    if (head_dim == 128) hipLaunchKernelGGL(norm_rope_dw_kernel<128>, dim3(16), dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL(norm_rope_dw_kernel<64>, dim3(8), dim3(1024), 0, stream, a);
   }
   return check_launch(fn);
 }
