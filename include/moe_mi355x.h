@@ -852,6 +852,11 @@ int moe_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ld, const void* dk_out,
                          void* dk, int64_t dk_ld, float* dw_q, float* dw_k, void* ws,
                          size_t ws_bytes, hipStream_t stream);
 
+/* moe_gqa_attn_fwd_workspace — bytes of moe_gqa_attn_fwd's workspace; it does
+ * not shrink as Tq grows, so one for the largest call serves all (0 for bad
+ * sizes and for Tq == 0). */
+size_t moe_gqa_attn_fwd_workspace(int Tq, int n_heads, int head_dim);
+
 /*
  * moe_gqa_attn_fwd — attention over packed sequences (prompts, training):
  *   s[i, j] = scale * q[i, h] . k[j, h / G]
@@ -869,7 +874,8 @@ int moe_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ld, const void* dk_out,
 int moe_gqa_attn_fwd(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v,
                      int64_t v_ld, int fmt, const int32_t* cu_q, const int32_t* cu_k, int B,
                      int Tq, int Tk, int n_heads, int n_kv_heads, int head_dim, int causal,
-                     float scale, void* out, int64_t out_ld, float* lse, hipStream_t stream);
+                     float scale, void* out, int64_t out_ld, float* lse, void* ws,
+                     size_t ws_bytes, hipStream_t stream);
 
 /* moe_gqa_attn_bwd_workspace — bytes of moe_gqa_attn_bwd's workspace; it does
  * not shrink as Tq or Tk grow, so one for the largest call serves all (0 for

@@ -25,8 +25,9 @@ from ._lib import (  # noqa: F401
     moe_grouped_fc2_nvfp4,
     moe_mla_attn_fwd, moe_mla_attn_bwd, moe_mla_attn_bwd_workspace, moe_mla_append, moe_mla_decode,
     moe_mla_decode_workspace,
-    moe_qk_norm_rope, moe_qk_norm_rope_bwd, moe_qk_norm_rope_bwd_workspace, moe_gqa_attn_fwd, moe_gqa_attn_bwd,
-    moe_gqa_attn_bwd_workspace, moe_gqa_append, moe_gqa_decode, moe_gqa_decode_workspace,
+    moe_qk_norm_rope, moe_qk_norm_rope_bwd, moe_qk_norm_rope_bwd_workspace, moe_gqa_attn_fwd,
+    moe_gqa_attn_fwd_workspace, moe_gqa_attn_bwd, moe_gqa_attn_bwd_workspace, moe_gqa_append, moe_gqa_decode,
+    moe_gqa_decode_workspace,
     SIGNATURES, LIB_PATH,
 )
 from .layer import (MoEForward, MoEBackward, RouterBackward, ExpertWeights, bias_update,  # noqa: F401

@@ -72,8 +72,9 @@ SIGNATURES = {
     "moe_qk_norm_rope_bwd_workspace": (_SZ, [_I]),
     "moe_qk_norm_rope_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _F, _P, _P, _I, _P,
                                   _I, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]),
+    "moe_gqa_attn_fwd_workspace": (_SZ, [_I, _I, _I]),
     "moe_gqa_attn_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P,
-                              _I64, _P, _P]),
+                              _I64, _P, _P, _SZ, _P]),
     "moe_gqa_attn_bwd_workspace": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_gqa_attn_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _P, _I64, _P, _P, _P, _I, _I, _I,
                               _I, _I, _I, _I, _F, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P]),
@@ -409,11 +410,16 @@ def moe_qk_norm_rope_bwd(dq_out, dqo_ld, dk_out, dko_ld, q, q_ld, k, k_ld, fmt, 
         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
+def moe_gqa_attn_fwd_workspace(Tq, n_heads, head_dim) -> int:
+    return load().moe_gqa_attn_fwd_workspace(Tq, n_heads, head_dim)
+
+
 def moe_gqa_attn_fwd(q, q_ld, k, k_ld, v, v_ld, fmt, cu_q, cu_k, B, Tq, Tk, n_heads, n_kv_heads,
-                     head_dim, causal, scale, out, out_ld, lse, stream=None):
+                     head_dim, causal, scale, out, out_ld, lse, ws, stream=None):
     _check("moe_gqa_attn_fwd", load().moe_gqa_attn_fwd(
         _ptr(q), q_ld, _ptr(k), k_ld, _ptr(v), v_ld, fmt, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, n_heads,
-        n_kv_heads, head_dim, causal, scale, _ptr(out), out_ld, _ptr(lse), _stream(stream)))
+        n_kv_heads, head_dim, causal, scale, _ptr(out), out_ld, _ptr(lse), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def moe_gqa_attn_bwd_workspace(Tq, Tk, n_heads, n_kv_heads, head_dim) -> int:

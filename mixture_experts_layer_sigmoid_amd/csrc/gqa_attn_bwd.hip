@@ -54,6 +54,7 @@ struct BwdArgs {
   float* part;            // [parts, Tk, nkv, 2, D]: dk (not scaled) and dv of each part
   int parts;
   int k_tiles, q_tiles;   // workgroups per key head (and part) of the two kinds
+  int q_first;            // dq's workgroups come first
 };
 
 // D / 8 lanes per (token, head) row
@@ -460,22 +461,24 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
                    r0 + wave * 32, n_rows, lane);
 }
 
-// Both kinds in one launch, dk / dv first: the second fills the compute units
-// that the first's last workgroups leave. Heads run fastest (an XCD keeps to
-// its own where their number is a multiple of 8); the tiles that see most come
-// first.
+// Both kinds in one launch: the second fills the compute units that the
+// first's last workgroups leave, and short sequences need both to fill the
+// chip. The kind whose workgroups walk more tiles comes first. Heads run
+// fastest (an XCD keeps to its own where their number is a multiple of 8); the
+// tiles that see most come first. A compute unit has one wave a SIMD with 128
+// values a head, two with 64.
 template <int D>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, 1)))
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(3 - D / 64, 3 - D / 64)))
 void bwd_kernel(BwdArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * stage_bytes<D>()];
-  const int n_kv = p.k_tiles * p.nkv * p.parts;
+  const int n_kv = p.k_tiles * p.nkv * p.parts, n_q = p.q_tiles * p.nkv;
   const int id = blockIdx.x;
   const int head = id % p.nkv;
-  if (id < n_kv) {
-    const int r = id / p.nkv;
+  if (p.q_first ? id >= n_q : id < n_kv) {
+    const int r = (p.q_first ? id - n_q : id) / p.nkv;
     bwd_kv<D>(p, head, r % p.parts, r / p.parts, smem);
   } else {
-    bwd_q<D>(p, head, p.q_tiles - 1 - (id - n_kv) / p.nkv, smem);
+    bwd_q<D>(p, head, p.q_tiles - 1 - (p.q_first ? id : id - n_kv) / p.nkv, smem);
   }
 }
 
@@ -508,17 +511,18 @@ __global__ __launch_bounds__(256) void bwd_join_kernel(BwdArgs p) {
 
 // Parts that the rows of a key tile are cut into: enough workgroups for two a
 // compute unit, as far as a part keeps 4 tiles of rows in the mean.
+constexpr int kMaxParts = 32;
 int parts_of(int Tq, int Tk, int nh, int nkv) {
   const int64_t wgs = (static_cast<int64_t>(Tk) + kSide - 1) / kSide * nkv;
   const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (4 * kTile);
   int64_t n = 2 * kNumCu / (wgs > 0 ? wgs : 1);
   n = n < tiles ? n : tiles;
-  return n < 1 ? 1 : (n > 16 ? 16 : static_cast<int>(n));
+  return n < 1 ? 1 : (n > kMaxParts ? kMaxParts : static_cast<int>(n));
 }
 // Rows of the parts' sums: parts_of never brings them above either bound, and
 // both grow with the sizes, so a workspace serves every smaller call.
 size_t part_rows(int Tk, int nkv) {
-  const size_t all = size_t{16} * Tk * nkv, most = size_t{2} * kNumCu * kSide;
+  const size_t all = size_t{kMaxParts} * Tk * nkv, most = size_t{2} * kNumCu * kSide;
   return all < most ? all : most;
 }
 size_t stats_bytes(int Tq, int nh) { return (static_cast<size_t>(Tq) * nh * 8 + 255) & ~size_t{255}; }
@@ -596,6 +600,7 @@ extern "C" int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q
   a.parts = parts_of(Tq, Tk, n_heads, n_kv_heads);
   a.k_tiles = Tk > 0 ? Tk / kSide + (B < Tk ? B : Tk) : 0;
   a.q_tiles = Tq > 0 ? Tq * a.g.d / kSide + (B < Tq ? B : Tq) : 0;
+  a.q_first = static_cast<int64_t>(Tq) * a.g.d / a.parts < Tk;
   if (head_dim == 128) launch_bwd<128>(a, stream);
   else launch_bwd<64>(a, stream);
   return check_launch(fn);

@@ -35,12 +35,15 @@ struct FwdArgs {
   int64_t out_ld;
   float* lse;
   int n_tiles;
+  int parts;               // of a sequence's keys, each a workgroup's
+  float* part;             // [parts, Tq, nh, D]: sums of each part, not normalized
+  float2* part_ml;         // [parts, Tq, nh]: their (reference, sum of weights)
 };
 
 constexpr int kKt = 64;                                  // keys per tile
 constexpr int NW = 4;                                    // waves, 32 rows each
 
-template <int D>
+template <int D, bool kParts>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void attn_fwd_kernel(FwdArgs p) {
   constexpr int kQt = 32 * NW;
@@ -55,7 +58,9 @@ void attn_fwd_kernel(FwdArgs p) {
   // (or a multiple) an XCD keeps to its own; later tiles of a sequence see
   // more keys and come first
   const int head = blockIdx.x % p.nkv;
-  const SeqTile st = find_rows(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, p.g.d, kQt, p.n_tiles - 1 - blockIdx.x / p.nkv);
+  const int index = blockIdx.x / p.nkv, part = kParts ? index % p.parts : 0;
+  const SeqTile st = find_rows(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, p.g.d, kQt,
+                               p.n_tiles - 1 - (kParts ? index / p.parts : index));
   if (st.b < 0) return;
   const int k_start = st.start2, n_k = st.n2;
   const int n_rows = st.n, n_q = quot(n_rows, p.g);
@@ -72,7 +77,9 @@ void attn_fwd_kernel(FwdArgs p) {
   const int last = p.causal ? min(tok + shift, n_k - 1) : n_k - 1;
   const int wave_first = last_of(r0), wave_last = last_of(r0 + 31);
   const int tile_last = last_of(st.tile * kQt + kQt - 1);
-  const int n_kt = tile_last < 0 ? 0 : tile_last / kKt + 1;
+  const int n_all = tile_last < 0 ? 0 : tile_last / kKt + 1;     // tiles of keys that some row sees
+  const int first_kt = kParts ? static_cast<int>(static_cast<int64_t>(n_all) * part / p.parts) : 0;
+  const int n_kt = kParts ? static_cast<int>(static_cast<int64_t>(n_all) * (part + 1) / p.parts) : n_all;
 
   const uint16_t* kb = p.k + static_cast<int64_t>(k_start) * p.k_ld + head * D;
   const uint16_t* vb = p.v + static_cast<int64_t>(k_start) * p.v_ld + head * D;
@@ -84,7 +91,7 @@ void attn_fwd_kernel(FwdArgs p) {
     tile_load<RB, kKt, NW>(vb + static_cast<int64_t>(kt) * kKt * p.v_ld, static_cast<uint32_t>(p.v_ld * 2), nv,
                            buf + kTileK, wave, lane);
   };
-  if (n_kt > 0) load(0, smem);
+  if (first_kt < n_kt) load(first_kt, smem);
 
   bf16x8_t qf[D / 16];
   {
@@ -106,11 +113,11 @@ void attn_fwd_kernel(FwdArgs p) {
   float m = -INFINITY, l = 0.f;
   const float c2 = p.scale * kLog2e;
 
-  for (int kt = 0; kt < n_kt; ++kt) {
+  for (int kt = first_kt; kt < n_kt; ++kt) {
     wait_vmcnt<0>();
     lds_barrier();
-    uint8_t* buf = smem + (kt & 1) * kTileBytes;
-    if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1) & 1) * kTileBytes);
+    uint8_t* buf = smem + ((kt - first_kt) & 1) * kTileBytes;
+    if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1 - first_kt) & 1) * kTileBytes);
     const int t0 = kt * kKt;
     if (t0 > wave_last) continue;          // nothing of this tile is visible to the wave
     f32x16_t s[2];
@@ -166,6 +173,19 @@ void attn_fwd_kernel(FwdArgs p) {
       }
   }
   l += other_half(l);
+  if constexpr (kParts) {
+    if (row < n_rows) {
+      const int64_t at = (static_cast<int64_t>(part) * p.Tq + st.start + tok) * p.nh + head * p.g.d + sub;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4_t*>(p.part + at * D + 32 * c + 8 * i + 4 * g) =
+              f32x4_t{o[c][4 * i], o[c][4 * i + 1], o[c][4 * i + 2], o[c][4 * i + 3]};
+      if (g == 0) p.part_ml[at] = make_float2(m, l);
+    }
+    return;
+  }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   lds_barrier();                        // everyone is done with the tiles
   uint8_t* rows = smem + wave * result_bytes<RB>();
@@ -182,14 +202,83 @@ void attn_fwd_kernel(FwdArgs p) {
         l == 0.f ? -INFINITY : fmaf(m, p.scale, log2_hw(l) * kLn2);
 }
 
+// ---- joining the parts of the keys, in order -----------------------------------
+// D / 4 lanes a row; only rows that a sequence holds.
+template <int D>
+__global__ __launch_bounds__(256) void fwd_join_kernel(FwdArgs p) {
+  constexpr int kL = D / 4;
+  const int lo = clamp_int(p.cu_q[0], 0, p.Tq), hi = clamp_int(p.cu_q[p.B], lo, p.Tq);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / kL) + threadIdx.x / kL;
+  const int64_t t = row / p.nh;
+  if (t < lo || t >= hi) return;
+  const int d = (threadIdx.x & (kL - 1)) * 4;
+  const int64_t step = static_cast<int64_t>(p.Tq) * p.nh;
+  const float c2 = p.scale * kLog2e;
+  float ref = -INFINITY;
+  for (int i = 0; i < p.parts; ++i) ref = fmaxf(ref, p.part_ml[row + i * step].x);
+  const float rc = ref == -INFINITY ? 0.f : ref * c2;
+  f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < p.parts; ++i) {
+    const float2 y = p.part_ml[row + i * step];
+    const f32x4_t z = *reinterpret_cast<const f32x4_t*>(p.part + (row + i * step) * D + d);
+    const float a = exp2_hw(fmaf(y.x, c2, -rc));
+    sum = fmaf(y.y, a, sum);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = fmaf(z[j], a, x[j]);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  const int h = static_cast<int>(row - t * p.nh);
+  *reinterpret_cast<uint2*>(p.out + t * p.out_ld + h * D + d) = pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  if (p.lse && d == 0) p.lse[row] = sum == 0.f ? -INFINITY : fmaf(ref, p.scale, log2_hw(sum) * kLn2);
+}
+
+// Parts that the keys are cut into: few rows leave compute units without a
+// workgroup, then as many as fill two a unit, of at least 6 tiles in the mean
+// (16 tokens x 64 heads over 8000 keys 141 us in one part, 30 in parts of 8
+// tiles, 53 in parts of 2).
+constexpr int kMaxParts = 64;
+int parts_of(int B, int Tq, int Tk, int nh, int nkv) {
+  const int64_t wgs = (static_cast<int64_t>(Tq) * (nh / nkv) + 32 * NW - 1) / (32 * NW) * nkv;
+  const int64_t tiles = static_cast<int64_t>(Tk) / B / (6 * kKt);
+  int64_t n = 2 * kNumCu / (wgs > 0 ? wgs : 1);
+  n = n < tiles ? n : tiles;
+  return n < 2 ? 1 : (n > kMaxParts ? kMaxParts : static_cast<int>(n));
+}
+// Rows of the parts' sums: never above either bound, and both grow with Tq, so
+// a workspace serves every smaller call.
+size_t part_rows(int Tq, int nh) {
+  const size_t all = size_t{kMaxParts} * Tq * nh, most = size_t{2} * kNumCu * 32 * NW;
+  return all < most ? all : most;
+}
+
+template <int D>
+void launch_fwd(const FwdArgs& a, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.n_tiles) * a.nkv * a.parts);
+  if (a.parts == 1) {
+    hipLaunchKernelGGL((attn_fwd_kernel<D, false>), grid, dim3(64 * NW), 0, stream, a);
+    return;
+  }
+  hipLaunchKernelGGL((attn_fwd_kernel<D, true>), grid, dim3(64 * NW), 0, stream, a);
+  constexpr int kPer = 256 / (D / 4);
+  const int64_t rows = static_cast<int64_t>(a.Tq) * a.nh;
+  hipLaunchKernelGGL(fwd_join_kernel<D>, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)), dim3(256), 0, stream, a);
+}
+
 }  // namespace
 }  // namespace gqa
 }  // namespace moe
 
+extern "C" size_t moe_gqa_attn_fwd_workspace(int Tq, int n_heads, int head_dim) {
+  if (Tq < 0 || Tq > (1 << 27) || n_heads < 1 || n_heads > 1024 || (head_dim != 64 && head_dim != 128)) return 0;
+  return moe::gqa::part_rows(Tq, n_heads) * (static_cast<size_t>(head_dim) * 4 + 8);
+}
+
 extern "C" int moe_gqa_attn_fwd(const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
                                 int fmt, const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk, int n_heads,
                                 int n_kv_heads, int head_dim, int causal, float scale, void* out, int64_t out_ld,
-                                float* lse, hipStream_t stream) {
+                                float* lse, void* ws, size_t ws_bytes, hipStream_t stream) {
   using namespace moe;
   using namespace moe::gqa;
   clear_error();
@@ -204,14 +293,19 @@ extern "C" int moe_gqa_attn_fwd(const void* q, int64_t q_ld, const void* k, int6
   if (B == 0 || Tq == 0) return MOE_OK;
   MOE_REQUIRE(q && cu_q && cu_k && out && (Tk == 0 || (k && v)), MOE_ERR_INVALID_ARG,
               "moe_gqa_attn_fwd: null pointer");
-  MOE_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out), MOE_ERR_ALIGNMENT,
-              "moe_gqa_attn_fwd: q, k, v and out must be 16-byte aligned");
+  MOE_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out) && aligned16(ws), MOE_ERR_ALIGNMENT,
+              "moe_gqa_attn_fwd: q, k, v, out and ws must be 16-byte aligned");
+  const size_t need = moe_gqa_attn_fwd_workspace(Tq, n_heads, head_dim);
+  MOE_REQUIRE(ws && ws_bytes >= need, MOE_ERR_WORKSPACE,
+              "moe_gqa_attn_fwd: ws smaller than moe_gqa_attn_fwd_workspace(Tq, n_heads, head_dim)");
   FwdArgs a{static_cast<const uint16_t*>(q), q_ld, static_cast<const uint16_t*>(k), k_ld,
             static_cast<const uint16_t*>(v), v_ld, cu_q, cu_k, B, Tq, Tk, n_heads, n_kv_heads, causal,
-            make_div(n_heads / n_kv_heads), scale, static_cast<uint16_t*>(out), out_ld, lse, 0};
+            make_div(n_heads / n_kv_heads), scale, static_cast<uint16_t*>(out), out_ld, lse, 0, 1, nullptr, nullptr};
   a.n_tiles = Tq * a.g.d / (32 * NW) + (B < Tq ? B : Tq);
-  const dim3 grid(static_cast<unsigned>(a.n_tiles) * n_kv_heads);
-  if (head_dim == 128) hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(64 * NW), 0, stream, a);
-  else hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(64 * NW), 0, stream, a);
+  a.parts = parts_of(B, Tq, Tk, n_heads, n_kv_heads);
+  a.part = static_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(a.part + part_rows(Tq, n_heads) * head_dim);
+  if (head_dim == 128) launch_fwd<128>(a, stream);
+  else launch_fwd<64>(a, stream);
   return check_launch(fn);
 }

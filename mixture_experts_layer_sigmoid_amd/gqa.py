@@ -153,7 +153,7 @@ class GroupedAttention:
     sequence's last query sees all its keys, each earlier one a key less.
     scale defaults to head_dim ** -0.5. Outputs are views of the object's
     buffers, as many rows as the call's inputs have; backward=True adds the
-    gradients' buffers and workspace."""
+    gradients' buffers and workspace. One object's calls must not overlap."""
 
     def __init__(self, *, Tq, Tk, n_heads, n_kv_heads, head_dim=128, n_seqs, causal=True, scale=None, backward=False,
                  device="cuda"):
@@ -164,13 +164,14 @@ class GroupedAttention:
         bf = dict(dtype=torch.bfloat16, device=device)
         self.out = torch.empty((Tq, n_heads, head_dim), **bf)
         self.lse = torch.empty((Tq, n_heads), dtype=torch.float32, device=device)
+        need = L.moe_gqa_attn_fwd_workspace(Tq, n_heads, head_dim)
         self.has_backward = backward
         if backward:
             self.dq = torch.empty_like(self.out)
             self.dk = torch.empty((Tk, n_kv_heads, head_dim), **bf)
             self.dv = torch.empty_like(self.dk)
-            self.ws = torch.empty((max(1, L.moe_gqa_attn_bwd_workspace(Tq, Tk, n_heads, n_kv_heads, head_dim)),),
-                                  dtype=torch.uint8, device=device)
+            need = max(need, L.moe_gqa_attn_bwd_workspace(Tq, Tk, n_heads, n_kv_heads, head_dim))
+        self.ws = torch.empty((max(1, need),), dtype=torch.uint8, device=device)
 
     def _inputs(self, q, k, v, cu_q, cu_k):
         h, kv, d = self.n_heads, self.n_kv_heads, self.head_dim
@@ -191,7 +192,7 @@ class GroupedAttention:
         ins, B, Tq, Tk, _ = self._inputs(q, k, v, cu_q, cu_k)
         h, d = self.n_heads, self.head_dim
         L.moe_gqa_attn_fwd(*ins, cu_q, cu_k, B, Tq, Tk, h, self.n_kv_heads, d, self.causal, self.scale, self.out,
-                           h * d, self.lse, stream)
+                           h * d, self.lse, self.ws, stream)
         return _first(self.out, Tq), _first(self.lse, Tq)
 
     __call__ = forward

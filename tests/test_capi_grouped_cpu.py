@@ -31,7 +31,7 @@ def _norm_bwd(lib, **k):
 
 def _fwd(lib, **k):
     a = dict(q=A, q_ld=256, k=A, k_ld=128, v=A, v_ld=128, fmt=1, cq=A, ck=A, B=1, Tq=4, Tk=4, h=2, kv=1, d=128,
-             causal=1, scale=1.0, out=A, out_ld=256, lse=None) | k
+             causal=1, scale=1.0, out=A, out_ld=256, lse=None, ws=A, wsb=BIG) | k
     return lib.moe_gqa_attn_fwd(*a.values(), None)
 
 
@@ -101,6 +101,15 @@ def test_attention_refusals(lib, call):
     assert b"moe_gqa_attn" in lib.moe_last_error()
     assert call(lib, B=0) == OK
     assert call(lib, Tq=0, Tk=0, q=None, k=None, v=None, out=None) == OK
+
+
+def test_attention_forward_workspace(lib):
+    need = lib.moe_gqa_attn_fwd_workspace(4, 2, 128)
+    assert _fwd(lib, wsb=need - 1) == WS and _fwd(lib, ws=None) == WS and _fwd(lib, ws=A + 8) == ALIGN
+    for bad in ((-1, 2, 128), (4, 0, 128), (4, 2, 96), (0, 2, 64)):
+        assert lib.moe_gqa_attn_fwd_workspace(*bad) == 0
+    sizes = [lib.moe_gqa_attn_fwd_workspace(t, 6, 64) for t in (0, 1, 2, 90, 200, 5000, 1 << 20)]
+    assert sizes == sorted(sizes)
 
 
 def test_attention_backward_refusals(lib):

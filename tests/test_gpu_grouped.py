@@ -176,6 +176,9 @@ PACKED = [
     (14, 2, 64, [200], [201], False),
     (24, 2, 128, [129, 20], [129, 84], True),         # groups of 12
     (3, 1, 128, [320], [320], True),                  # the backward's rows in parts
+    (8, 2, 64, [3, 20], [1500, 700], True),           # the forward's keys in parts
+    (2, 1, 128, [1, 5, 2], [2100, 0, 3], False),      # parts without keys
+    (12, 4, 128, [40, 7], [900, 600], False),
 ]
 
 
@@ -248,7 +251,8 @@ def test_attention_strides_outside_rows_and_hidden_nan(gpu_lib):
     ws = torch.empty(L.moe_gqa_attn_bwd_workspace(T, T, h, kv, d), dtype=torch.uint8, device="cuda")
     ld = lambda t: t.stride(0)
     heads = (1, cu, cu, 2, T, T, h, kv, d, 1, d ** -0.5)
-    L.moe_gqa_attn_fwd(wq, ld(wq), wk, ld(wk), wv, ld(wv), *heads, out, ld(out), lse)
+    fws = torch.empty(L.moe_gqa_attn_fwd_workspace(T, h, d), dtype=torch.uint8, device="cuda")
+    L.moe_gqa_attn_fwd(wq, ld(wq), wk, ld(wk), wv, ld(wv), *heads, out, ld(out), lse, fws)
     dq, dk, dv = cut(dqkv, 0, h), cut(dqkv, h * d, kv), cut(dqkv, (h + kv) * d, kv)
     L.moe_gqa_attn_bwd(wdo, ld(wdo), wq, ld(wq), wk, ld(wk), wv, ld(wv), 1, out, ld(out), lse, *heads[1:], dq, ld(dq),
                        dk, ld(dk), dv, ld(dv), ws)
