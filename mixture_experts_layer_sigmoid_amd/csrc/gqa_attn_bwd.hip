@@ -132,9 +132,11 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   const int shift = p.causal ? n_k - n_q : n_k;                // query i sees keys <= i + shift
   auto first_row = [&](int j) { return clamp_int(j - shift, 0, n_q) * p.g.d; };   // that sees key j
   const int t_lo = first_row(k0) / kTile, t_hi = (n_rows + kTile - 1) / kTile;
-  const int n_t = t_hi > t_lo ? t_hi - t_lo : 0;
-  const int t_first = t_lo + static_cast<int>(static_cast<int64_t>(n_t) * part / p.parts);
-  const int t_end = t_lo + static_cast<int>(static_cast<int64_t>(n_t) * (part + 1) / p.parts);
+  // Row tiles are taken from the last one down, every parts-th: all workgroups
+  // of a head, whose first rows differ, start with the same ones and meet them
+  // in the XCD's L2.
+  const int t_top = t_hi - 1 - part;
+  const int n_t = t_top >= t_lo ? (t_top - t_lo) / p.parts + 1 : 0;
   const int row_min = first_row(keyc);                         // rows before it do not see this lane's key
 
   const uint16_t* q = p.q + static_cast<int64_t>(q_start) * p.q_ld + head * p.g.d * D;
@@ -157,7 +159,7 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
       s[64 + lane] = stat_next.y;
     }
   };
-  if (t_first < t_end) load(t_first, smem);
+  if (n_t > 0) load(t_top, smem);
 
   bf16x8_t kf[S], vf[S];
   {
@@ -180,13 +182,14 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   }
   const float c2 = p.scale * kLog2e;
 
-  auto tile = [&](int t, auto cut_c) {
+  auto tile = [&](int i, auto cut_c) {
     constexpr bool kCut = decltype(cut_c)::value;
-    uint8_t* buf = smem + ((t - t_first) & 1) * kStage;
+    const int t = t_top - i * p.parts;
+    uint8_t* buf = smem + (i & 1) * kStage;
     put_stats(buf);                   // the other buffer's readers are a barrier behind
     wait_vmcnt<0>();
     lds_barrier();
-    if (t + 1 < t_end) load(t + 1, smem + ((t + 1 - t_first) & 1) * kStage);
+    if (i + 1 < n_t) load(t - p.parts, smem + ((i + 1) & 1) * kStage);
     const float* stat = reinterpret_cast<const float*>(buf + kStat);
     // 8 S products of two blocks of 32 rows: the scores and dp of block 0, of
     // block 1, then dv and dk from block 0 and from block 1. Their LDS
@@ -270,14 +273,14 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
       keep_acc(dk[c]);
       keep_acc(dv[c]);
     }
-    ops.move((t - t_first) & 1 ? -kStage : kStage);
+    ops.move(i & 1 ? -kStage : kStage);
   };
-  // the tiles that the causal mask cuts come first; each loop has one body
-  const int cut_hi = p.causal ? (first_row(min(k0 + kSide, n_k) - 1) + kTile - 1) / kTile : t_first;
-  const int cut_end = min(t_end, max(t_first, cut_hi));
-  int t = t_first;
-  for (; t < cut_end; ++t) tile(t, std::true_type{});
-  for (; t < t_end; ++t) tile(t, std::false_type{});
+  // the tiles that the causal mask cuts come last; each loop has one body
+  const int cut_hi = p.causal ? (first_row(min(k0 + kSide, n_k) - 1) + kTile - 1) / kTile : 0;
+  const int n_whole = t_top >= cut_hi ? min(n_t, (t_top - cut_hi) / p.parts + 1) : 0;
+  int i = 0;
+  for (; i < n_whole; ++i) tile(i, std::false_type{});
+  for (; i < n_t; ++i) tile(i, std::true_type{});
   acc_settled();
   lds_barrier();                        // everyone is done with the tiles
   auto value = [&](const f32x16_t& x, int i) {
