@@ -83,38 +83,24 @@ __global__ __launch_bounds__(256) void bwd_stats_kernel(BwdArgs p) {
   }
 }
 
-// LDS offsets of the operands of one stage: a tile of RB-byte rows, and a
-// second one behind it that is read with the first's offsets. They move with
-// the stage in use, so no address is computed between the products.
-template <int RB>
-struct Operands {
-  uint32_t row[RB / 32], col[RB / 64][2];
-  __device__ __forceinline__ explicit Operands(int lane) {
-#pragma unroll
-    for (int s = 0; s < RB / 32; ++s) row[s] = row_operand_offset<RB>(lane, s);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < RB / 64; ++c) col[c][h] = col_operand_offset<RB>(lane, c, h);
-  }
-  __device__ __forceinline__ void move(int by) {
-#pragma unroll
-    for (int s = 0; s < RB / 32; ++s) row[s] += by;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < RB / 64; ++c) col[c][h] += by;
-  }
-};
-
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 constexpr int kTile = 64;                               // rows or keys that pass by at a time
-constexpr int kSide = 32 * kWaves;                      // keys or rows that a workgroup keeps
-constexpr int kAhead = 5;                               // matrix operands read ahead
+constexpr int kKeys = 16 * kWaves;                      // keys that a workgroup keeps: 32 a pair of waves
+constexpr int kKept = 32 * kWaves;                      // packed rows that a workgroup keeps
 template <int D>
 constexpr int stage_bytes() { return 2 * kTile * D * 2 + kTile * 8; }
+constexpr int kPass = 64 * 4 * 16;                      // weights of 32 x 32 in fp32
+constexpr int kPassAll = kWaves / 2 * 2 * kPass;
+template <int D>
+constexpr int smem_bytes() { return 2 * stage_bytes<D>() + kPassAll; }
 
-// ---- dk, dv: a wave keeps 32 keys (the lanes' columns), packed rows pass by ----
+// ---- dk, dv: a pair of waves keeps 32 keys (the lanes' columns), rows pass by ---
+// The first wave of a pair has the keys: scores, weights, dv = p^T do. The
+// second has their values: dp, ds with the weights that the first left in LDS
+// (fp32, as they lie in its accumulator), dk = ds^T q. So both take the same
+// steps on the two tiles the other way round, and a wave's operands and sums
+// leave room for two waves a SIMD, of which one has products while the other
+// has elements.
 template <int D>
 __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int tile_index, uint8_t* smem) {
   constexpr int RB = D * 2, S = D / 16, C = D / 32;
@@ -122,12 +108,14 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   constexpr int kStat = 2 * kTile * RB, kStage = stage_bytes<D>();
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const SeqTile st = find_rows(p.cu_k, p.cu_q, p.B, p.Tk, p.Tq, 1, kSide, tile_index);
+  const int pair = wave & (kWaves / 2 - 1);
+  const bool has_keys = wave < kWaves / 2;
+  const SeqTile st = find_rows(p.cu_k, p.cu_q, p.B, p.Tk, p.Tq, 1, kKeys, tile_index);
   if (st.b < 0) return;
   const int n_k = st.n;
   const int q_start = st.start2, n_q = st.n2, n_rows = n_q * p.g.d;
-  const int k0 = st.tile * kSide;
-  const int key = k0 + wave * 32 + (lane & 31);
+  const int k0 = st.tile * kKeys;
+  const int key = k0 + pair * 32 + (lane & 31);
   const int keyc = key < n_k ? key : n_k - 1;
   const int shift = p.causal ? n_k - n_q : n_k;                // query i sees keys <= i + shift
   auto first_row = [&](int j) { return clamp_int(j - shift, 0, n_q) * p.g.d; };   // that sees key j
@@ -161,28 +149,28 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   };
   if (n_t > 0) load(t_top, smem);
 
-  bf16x8_t kf[S], vf[S];
+  bf16x8_t kept[S];
   {
     const int64_t tok = static_cast<int64_t>(st.start) + keyc;
-    const uint16_t* k = p.k + tok * p.k_ld + head * D + 8 * g;
-    const uint16_t* v = p.v + tok * p.v_ld + head * D + 8 * g;
+    const uint16_t* x = (has_keys ? p.k + tok * p.k_ld : p.v + tok * p.v_ld) + head * D + 8 * g;
 #pragma unroll
-    for (int s = 0; s < S; ++s) kf[s] = *reinterpret_cast<const bf16x8_t*>(k + 16 * s);
-#pragma unroll
-    for (int s = 0; s < S; ++s) vf[s] = *reinterpret_cast<const bf16x8_t*>(v + 16 * s);
+    for (int s = 0; s < S; ++s) kept[s] = *reinterpret_cast<const bf16x8_t*>(x + 16 * s);
   }
-  Operands<RB> ops(lane);
-  f32x16_t dk[C], dv[C];
+  // rows of Q or dO as they lie, columns of the other tile
+  uint32_t row_off[S], col_off[C][2];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    dk[c] = f32x16_t{};
-    keep_acc(dk[c]);
-    dv[c] = f32x16_t{};
-    keep_acc(dv[c]);
-  }
+  for (int s = 0; s < S; ++s) row_off[s] = row_operand_offset<RB>(lane, s) + (has_keys ? 0 : kDo);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) col_off[c][h] = col_operand_offset<RB>(lane, c, h) + (has_keys ? kDo : 0);
+  f32x4_t* pass = reinterpret_cast<f32x4_t*>(smem + 2 * kStage + pair * 2 * kPass) + lane;
+  f32x16_t sum[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) sum[c] = f32x16_t{};
   const float c2 = p.scale * kLog2e;
 
-  auto tile = [&](int i, auto cut_c) {
+  auto tile = [&](int i, auto cut_c) __attribute__((always_inline)) {
     constexpr bool kCut = decltype(cut_c)::value;
     const int t = t_top - i * p.parts;
     uint8_t* buf = smem + (i & 1) * kStage;
@@ -190,129 +178,83 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
     wait_vmcnt<0>();
     lds_barrier();
     if (i + 1 < n_t) load(t - p.parts, smem + ((i + 1) & 1) * kStage);
-    const float* stat = reinterpret_cast<const float*>(buf + kStat);
-    // 8 S products of two blocks of 32 rows: the scores and dp of block 0, of
-    // block 1, then dv and dk from block 0 and from block 1. Their LDS
-    // operands are read kAhead products ahead, and the element-wise work of
-    // block 0 runs between the products of block 1's scores, that of block 1
-    // between the products of block 0's gradients.
-    constexpr int kB = 2 * S, kN = 4 * kB;
-    bf16x8_t a[kAhead], pf[2][2], sf[2][2];
-    f32x16_t s[2], dp[2];
-    f32x4_t l2[2], dl[2];
-    typedef float f32x8_t __attribute__((ext_vector_type(8)));
-    f32x8_t we, de;                   // elements of the current operand
-    auto fetch = [&](auto n_c) {
-      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
-      if constexpr (n < 2 * kB) {
-        constexpr int b = n / kB, k = n % kB;
-        a[slot] = row_operand(smem, ops.row[k / 2] + (k % 2 ? kDo : 0) + b * 32 * RB);
-      } else {
-        constexpr int b = (n - 2 * kB) / kB, k = (n - 2 * kB) % kB / (2 * C), c = (n - 2 * kB) % (2 * C);
-        constexpr int o = (2 * b + k) * 16 * RB + (c < C ? kDo : 0);
-        a[slot] = col_operand(smem, ops.col[c % C][0] + o, ops.col[c % C][1] + o);
-      }
-    };
-    // statistics of 4 rows: elements 4 j .. 4 j + 3 of block b
-    auto stats_of = [&](auto b_c, auto j_c) {
-      constexpr int b = decltype(b_c)::value, j = decltype(j_c)::value;
-      l2[j & 1] = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j + 4 * g);
-      dl[j & 1] = *reinterpret_cast<const f32x4_t*>(stat + 64 + 32 * b + 8 * j + 4 * g);
-    };
-    auto element = [&](auto b_c, auto i_c) {
-      constexpr int b = decltype(b_c)::value, i = decltype(i_c)::value;
-      if constexpr (i % 4 == 0 && i < 12) stats_of(b_c, std::integral_constant<int, i / 4 + 1>{});
-      float w = exp2_hw(fmaf(s[b][i], c2, -l2[(i >> 2) & 1][i & 3]));
-      float d = w * (dp[b][i] - dl[(i >> 2) & 1][i & 3]);
-      if constexpr (kCut) {
-        const bool hidden = t * kTile + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) < row_min;
-        w = hidden ? 0.f : w;
-        d = hidden ? 0.f : d;
-      }
-      we[i % 8] = w;
-      de[i % 8] = d;
-      if constexpr (i % 8 == 7) {
-        pf[b][i / 8] = __builtin_convertvector(we, bf16x8_t);
-        sf[b][i / 8] = __builtin_convertvector(de, bf16x8_t);
-      }
-    };
-    // block b's 16 elements follow its scores at an even pace, all done before
-    // the products that take them
-    auto elements_behind = [&](auto b_c, auto n_c) {
-      constexpr int n = decltype(n_c)::value, b = decltype(b_c)::value;
-      constexpr int from = (b + 1) * kB + 2, room = kB - 4;
-      if constexpr (n >= from && n < from + room) {
-        constexpr int lo = 16 * (n - from) / room, hi = 16 * (n - from + 1) / room;
-        static_for<hi - lo>([&](auto i_c) {
-          element(b_c, std::integral_constant<int, lo + decltype(i_c)::value>{});
-        });
-      }
-    };
-    static_for<kAhead>([&](auto n_c) { fetch(n_c); });
-    __builtin_amdgcn_sched_barrier(0);
-    static_for<kN>([&](auto n_c) {
-      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
-      if constexpr (n < 2 * kB) {
-        constexpr int b = n / kB, k = n % kB;
-        if constexpr (k % 2 == 0) s[b] = mfma(a[slot], kf[k / 2], k == 0 ? f32x16_t{} : s[b]);
-        else dp[b] = mfma(a[slot], vf[k / 2], k == 1 ? f32x16_t{} : dp[b]);
-      } else {
-        constexpr int b = (n - 2 * kB) / kB, k = (n - 2 * kB) % kB / (2 * C), c = (n - 2 * kB) % (2 * C);
-        if constexpr (c < C) dv[c] = mfma(a[slot], pf[b][k], dv[c]);
-        else dk[c - C] = mfma(a[slot], sf[b][k], dk[c - C]);
-      }
-      if constexpr (n + kAhead < kN) fetch(std::integral_constant<int, n + kAhead>{});
-      if constexpr (n == kB - 2 || n == 2 * kB - 2)
-        stats_of(std::integral_constant<int, n / kB>{}, std::integral_constant<int, 0>{});
-      elements_behind(std::integral_constant<int, 0>{}, n_c);
-      elements_behind(std::integral_constant<int, 1>{}, n_c);
-      __builtin_amdgcn_sched_barrier(0);
-    });
+    const float* stat = reinterpret_cast<const float*>(buf + kStat) + 4 * g;
+    f32x16_t x[2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      keep_acc(dk[c]);
-      keep_acc(dv[c]);
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int k = 0; k < S; ++k)
+        x[b] = mfma(row_operand(buf, row_off[k] + b * 32 * RB), kept[k], k == 0 ? f32x16_t{} : x[b]);
+    if (has_keys) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4_t l2 = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j);
+          f32x4_t w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = exp2_hw(fmaf(x[b][4 * j + e], c2, -l2[e]));
+            if constexpr (kCut) w[e] = t * kTile + 32 * b + 8 * j + 4 * g + e < row_min ? 0.f : w[e];
+            x[b][4 * j + e] = w[e];
+          }
+          pass[(4 * b + j) * 64] = w;
+        }
+      lds_barrier();
+    } else {
+      lds_barrier();
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(stat + 64 + 32 * b + 8 * j);
+          const f32x4_t w = pass[(4 * b + j) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[b][4 * j + e] = w[e] * (x[b][4 * j + e] - delta[e]);
+        }
     }
-    ops.move(i & 1 ? -kStage : kStage);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bf16x8_t f = pack_operand(x[b], k);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          sum[c] = mfma(col_operand(buf, col_off[c][0] + (2 * b + k) * 16 * RB, col_off[c][1] + (2 * b + k) * 16 * RB),
+                        f, sum[c]);
+      }
   };
-  // the tiles that the causal mask cuts come last; each loop has one body
-  const int cut_hi = p.causal ? (first_row(min(k0 + kSide, n_k) - 1) + kTile - 1) / kTile : 0;
+  // the tiles that the causal mask cuts come last
+  const int cut_hi = p.causal ? (first_row(min(k0 + kKeys, n_k) - 1) + kTile - 1) / kTile : 0;
   const int n_whole = t_top >= cut_hi ? min(n_t, (t_top - cut_hi) / p.parts + 1) : 0;
   int i = 0;
   for (; i < n_whole; ++i) tile(i, std::false_type{});
   for (; i < n_t; ++i) tile(i, std::true_type{});
-  acc_settled();
+
   lds_barrier();                        // everyone is done with the tiles
-  auto value = [&](const f32x16_t& x, int i) {
-    return f32x4_t{read_acc(x[4 * i]), read_acc(x[4 * i + 1]), read_acc(x[4 * i + 2]), read_acc(x[4 * i + 3])};
-  };
-  const int64_t tok = static_cast<int64_t>(st.start) + k0 + wave * 32;
-  const int n_out = n_k - k0 - wave * 32;
-  static_assert(kWaves * result_bytes<RB>() <= 2 * kStage, "results fit the tile buffers");
-  uint8_t* rows = smem + wave * result_bytes<RB>();
+  const int64_t tok = static_cast<int64_t>(st.start) + k0 + pair * 32;
+  const int n_out = n_k - k0 - pair * 32;
+  static_assert(kWaves * result_bytes<RB>() <= smem_bytes<D>(), "results fit the tile buffers");
   if (p.parts == 1) {
-    auto put = [&](const f32x16_t* x, float sc, uint16_t* dst, int64_t ld) {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4_t y = value(x[c], i) * sc;
-          *reinterpret_cast<uint2*>(rows + (lane & 31) * (RB + 16) + (32 * c + 8 * i + 4 * g) * 2) =
-              pack4(y[0], y[1], y[2], y[3]);
-        }
-      store_rows<RB>(rows, dst + tok * ld + head * D, ld * 2, n_out, lane);
-    };
-    put(dk, p.scale, p.dk, p.dk_ld);
-    put(dv, 1.f, p.dv, p.dv_ld);
-  } else if ((lane & 31) < n_out) {
-    float* dst = p.part + (((static_cast<int64_t>(part) * p.Tk + tok + (lane & 31)) * p.nkv + head) * 2) * D + 4 * g;
+    uint8_t* rows = smem + wave * result_bytes<RB>();
+    const float sc = has_keys ? 1.f : p.scale;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        *reinterpret_cast<f32x4_t*>(dst + 32 * c + 8 * i) = value(dk[c], i);
-        *reinterpret_cast<f32x4_t*>(dst + D + 32 * c + 8 * i) = value(dv[c], i);
-      }
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint2*>(rows + (lane & 31) * (RB + 16) + (32 * c + 8 * j + 4 * g) * 2) =
+            pack4(sum[c][4 * j] * sc, sum[c][4 * j + 1] * sc, sum[c][4 * j + 2] * sc, sum[c][4 * j + 3] * sc);
+    const int64_t ld = has_keys ? p.dv_ld : p.dk_ld;
+    store_rows<RB>(rows, (has_keys ? p.dv : p.dk) + tok * ld + head * D, ld * 2, n_out, lane);
+  } else if ((lane & 31) < n_out) {
+    float* dst = p.part + (((static_cast<int64_t>(part) * p.Tk + tok + (lane & 31)) * p.nkv + head) * 2 +
+                           (has_keys ? 1 : 0)) * D + 4 * g;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4_t*>(dst + 32 * c + 8 * j) =
+            f32x4_t{sum[c][4 * j], sum[c][4 * j + 1], sum[c][4 * j + 2], sum[c][4 * j + 3]};
   }
 }
 
@@ -324,11 +266,11 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
   constexpr int kStage = stage_bytes<D>();
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const SeqTile st = find_rows(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, p.g.d, kSide, tile_index);
+  const SeqTile st = find_rows(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, p.g.d, kKept, tile_index);
   if (st.b < 0) return;
   const int k_start = st.start2, n_k = st.n2;
   const int n_rows = st.n, n_q = quot(n_rows, p.g);
-  const int r0 = st.tile * kSide;
+  const int r0 = st.tile * kKept;
   const int row = r0 + wave * 32 + (lane & 31);
   const int rowc = row < n_rows ? row : n_rows - 1;
   const int tok = quot(rowc, p.g), sub = rowc - tok * p.g.d;
@@ -337,7 +279,7 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
     return p.causal ? min(quot(min(r, n_rows - 1), p.g) + shift, n_k - 1) : n_k - 1;
   };
   const int last = p.causal ? min(tok + shift, n_k - 1) : n_k - 1;
-  const int first_last = last_of(r0), tile_last = last_of(r0 + kSide - 1);
+  const int first_last = last_of(r0), tile_last = last_of(r0 + kKept - 1);
   const int n_kt = tile_last < 0 ? 0 : tile_last / kTile + 1;
   const int n_full = first_last < 0 ? 0 : min(n_kt, (first_last + 1) / kTile);   // tiles that every row sees whole
 
@@ -365,90 +307,51 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
     for (int s = 0; s < S; ++s) df[s] = *reinterpret_cast<const bf16x8_t*>(d + 16 * s);
   }
   const float2 stat = p.stats[tokc * p.nh + h];
-  Operands<RB> ops(lane);
+  uint32_t row_off[S], col_off[C][2];
+#pragma unroll
+  for (int s = 0; s < S; ++s) row_off[s] = row_operand_offset<RB>(lane, s);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) col_off[c][k] = col_operand_offset<RB>(lane, c, k);
   f32x16_t dq[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    dq[c] = f32x16_t{};
-    keep_acc(dq[c]);
-  }
+  for (int c = 0; c < C; ++c) dq[c] = f32x16_t{};
   const float c2 = p.scale * kLog2e;
 
-  auto tile = [&](int kt, auto cut_c) {
+  auto tile = [&](int kt, auto cut_c) __attribute__((always_inline)) {
     constexpr bool kCut = decltype(cut_c)::value;
     wait_vmcnt<0>();
     lds_barrier();
+    uint8_t* buf = smem + (kt & 1) * kStage;
     if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1) & 1) * kStage);
-    // 6 S products, in the order of the kernel above: scores and dp of block 0
-    // and block 1 of 32 keys, then dq from block 0 and from block 1
-    constexpr int kB = 2 * S, kN = 2 * kB + 4 * C;
-    bf16x8_t a[kAhead], sf[2][2];
-    f32x16_t s[2], dp[2];
-    typedef float f32x8_t __attribute__((ext_vector_type(8)));
-    f32x8_t de;
-    auto fetch = [&](auto n_c) {
-      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
-      if constexpr (n < 2 * kB) {
-        constexpr int b = n / kB, k = n % kB;
-        a[slot] = row_operand(smem, ops.row[k / 2] + (k % 2 ? kV : 0) + b * 32 * RB);
-      } else {
-        constexpr int k = (n - 2 * kB) / C, c = (n - 2 * kB) % C;
-        a[slot] = col_operand(smem, ops.col[c][0] + k * 16 * RB, ops.col[c][1] + k * 16 * RB);
-      }
-    };
-    auto element = [&](auto b_c, auto i_c) {
-      constexpr int b = decltype(b_c)::value, i = decltype(i_c)::value;
-      float d = exp2_hw(fmaf(s[b][i], c2, -stat.x)) * (dp[b][i] - stat.y);
-      if constexpr (kCut) d = kt * kTile + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) > last ? 0.f : d;
-      de[i % 8] = d;
-      if constexpr (i % 8 == 7) sf[b][i / 8] = __builtin_convertvector(de, bf16x8_t);
-    };
-    // elements [8 part, 8 part + 8) of block b behind products [from, from + room)
-    auto elements_behind = [&](auto b_c, auto part_c, auto from_c, auto room_c, auto n_c) {
-      constexpr int n = decltype(n_c)::value, from = decltype(from_c)::value, room = decltype(room_c)::value;
-      if constexpr (n >= from && n < from + room) {
-        constexpr int lo = 8 * (n - from) / room, hi = 8 * (n - from + 1) / room;
-        static_for<hi - lo>([&](auto i_c) {
-          element(b_c, std::integral_constant<int, 8 * decltype(part_c)::value + lo + decltype(i_c)::value>{});
-        });
-      }
-    };
-    static_for<kAhead>([&](auto n_c) { fetch(n_c); });
-    __builtin_amdgcn_sched_barrier(0);
-    static_for<kN>([&](auto n_c) {
-      constexpr int n = decltype(n_c)::value, slot = n % kAhead;
-      if constexpr (n < 2 * kB) {
-        constexpr int b = n / kB, k = n % kB;
-        if constexpr (k % 2 == 0) s[b] = mfma(a[slot], qf[k / 2], k == 0 ? f32x16_t{} : s[b]);
-        else dp[b] = mfma(a[slot], df[k / 2], k == 1 ? f32x16_t{} : dp[b]);
-      } else {
-        constexpr int k = (n - 2 * kB) / C, c = (n - 2 * kB) % C;
-        dq[c] = mfma(a[slot], sf[k / 2][k % 2], dq[c]);
-      }
-      if constexpr (n + kAhead < kN) fetch(std::integral_constant<int, n + kAhead>{});
-      typedef std::integral_constant<int, 0> I0;
-      typedef std::integral_constant<int, 1> I1;
-      // block 0 behind block 1's scores; block 1's two halves each before
-      // their own products (k-steps 2 and 3)
-      constexpr int kHalf = kB / 2 - 1;
-      elements_behind(I0{}, I0{}, std::integral_constant<int, kB + 2>{}, std::integral_constant<int, kHalf>{}, n_c);
-      elements_behind(I0{}, I1{}, std::integral_constant<int, kB + 2 + kHalf>{},
-                      std::integral_constant<int, kB - 2 - kHalf>{}, n_c);
-      elements_behind(I1{}, I0{}, std::integral_constant<int, 2 * kB + 2 * C - (2 * C - 1)>{},
-                      std::integral_constant<int, 2 * C - 1>{}, n_c);
-      elements_behind(I1{}, I1{}, std::integral_constant<int, 2 * kB + 2 * C>{}, std::integral_constant<int, C>{},
-                      n_c);
-      __builtin_amdgcn_sched_barrier(0);
-    });
 #pragma unroll
-    for (int c = 0; c < C; ++c) keep_acc(dq[c]);
-    ops.move(kt & 1 ? -kStage : kStage);
+    for (int b = 0; b < 2; ++b) {
+      f32x16_t s, dp;
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        s = mfma(row_operand(buf, row_off[k] + b * 32 * RB), qf[k], k == 0 ? f32x16_t{} : s);
+        dp = mfma(row_operand(buf, row_off[k] + kV + b * 32 * RB), df[k], k == 0 ? f32x16_t{} : dp);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = exp2_hw(fmaf(s[i], c2, -stat.x)) * (dp[i] - stat.y);
+        if constexpr (kCut) s[i] = kt * kTile + 32 * b + 8 * (i >> 2) + 4 * g + (i & 3) > last ? 0.f : s[i];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bf16x8_t f = pack_operand(s, k);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          dq[c] = mfma(col_operand(buf, col_off[c][0] + (2 * b + k) * 16 * RB, col_off[c][1] + (2 * b + k) * 16 * RB),
+                       f, dq[c]);
+      }
+    }
   };
   int kt = 0;
   for (; kt < n_full; ++kt) tile(kt, std::false_type{});
   for (; kt < n_kt; ++kt) tile(kt, std::true_type{});
 
-  acc_settled();
   lds_barrier();                        // everyone is done with the tiles
   uint8_t* rows = smem + wave * result_bytes<RB>();
 #pragma unroll
@@ -457,8 +360,7 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
     for (int i = 0; i < 4; ++i) {
       const float sc = p.scale;
       *reinterpret_cast<uint2*>(rows + (lane & 31) * (RB + 16) + (32 * c + 8 * i + 4 * g) * 2) =
-          pack4(read_acc(dq[c][4 * i]) * sc, read_acc(dq[c][4 * i + 1]) * sc, read_acc(dq[c][4 * i + 2]) * sc,
-                read_acc(dq[c][4 * i + 3]) * sc);
+          pack4(dq[c][4 * i] * sc, dq[c][4 * i + 1] * sc, dq[c][4 * i + 2] * sc, dq[c][4 * i + 3] * sc);
     }
   store_packed<RB>(rows, p.dq + static_cast<int64_t>(st.start) * p.dq_ld + head * p.g.d * D, p.dq_ld, p.g,
                    r0 + wave * 32, n_rows, lane);
@@ -468,12 +370,11 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
 // first's last workgroups leave, and short sequences need both to fill the
 // chip. The kind whose workgroups walk more tiles comes first. Heads run
 // fastest (an XCD keeps to its own where their number is a multiple of 8); the
-// tiles that see most come first. A compute unit has one wave a SIMD with 128
-// values a head, two with 64.
+// tiles that see most come first.
 template <int D>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(3 - D / 64, 3 - D / 64)))
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void bwd_kernel(BwdArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * stage_bytes<D>()];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[smem_bytes<D>()];
   const int n_kv = p.k_tiles * p.nkv * p.parts, n_q = p.q_tiles * p.nkv;
   const int id = blockIdx.x;
   const int head = id % p.nkv;
@@ -516,7 +417,7 @@ __global__ __launch_bounds__(256) void bwd_join_kernel(BwdArgs p) {
 // compute unit, as far as a part keeps 4 tiles of rows in the mean.
 constexpr int kMaxParts = 32;
 int parts_of(int Tq, int Tk, int nh, int nkv) {
-  const int64_t wgs = (static_cast<int64_t>(Tk) + kSide - 1) / kSide * nkv;
+  const int64_t wgs = (static_cast<int64_t>(Tk) + kKeys - 1) / kKeys * nkv;
   const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (4 * kTile);
   int64_t n = 2 * kNumCu / (wgs > 0 ? wgs : 1);
   n = n < tiles ? n : tiles;
@@ -525,7 +426,7 @@ int parts_of(int Tq, int Tk, int nh, int nkv) {
 // Rows of the parts' sums: parts_of never brings them above either bound, and
 // both grow with the sizes, so a workspace serves every smaller call.
 size_t part_rows(int Tk, int nkv) {
-  const size_t all = size_t{kMaxParts} * Tk * nkv, most = size_t{2} * kNumCu * kSide;
+  const size_t all = size_t{kMaxParts} * Tk * nkv, most = size_t{2} * kNumCu * kKeys;
   return all < most ? all : most;
 }
 size_t stats_bytes(int Tq, int nh) { return (static_cast<size_t>(Tq) * nh * 8 + 255) & ~size_t{255}; }
@@ -601,8 +502,8 @@ extern "C" int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q
   a.stats = static_cast<float2*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + stats_bytes(Tq, n_heads));
   a.parts = parts_of(Tq, Tk, n_heads, n_kv_heads);
-  a.k_tiles = Tk > 0 ? Tk / kSide + (B < Tk ? B : Tk) : 0;
-  a.q_tiles = Tq > 0 ? Tq * a.g.d / kSide + (B < Tq ? B : Tq) : 0;
+  a.k_tiles = Tk > 0 ? Tk / kKeys + (B < Tk ? B : Tk) : 0;
+  a.q_tiles = Tq > 0 ? Tq * a.g.d / kKept + (B < Tq ? B : Tq) : 0;
   a.q_first = static_cast<int64_t>(Tq) * a.g.d / a.parts < Tk;
   if (head_dim == 128) launch_bwd<128>(a, stream);
   else launch_bwd<64>(a, stream);
