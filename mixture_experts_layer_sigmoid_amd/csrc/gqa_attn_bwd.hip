@@ -83,16 +83,24 @@ __global__ __launch_bounds__(256) void bwd_stats_kernel(BwdArgs p) {
   }
 }
 
-constexpr int kWaves = 8;
-constexpr int kTile = 64;                               // rows or keys that pass by at a time
-constexpr int kKeys = 16 * kWaves;                      // keys that a workgroup keeps: 32 a pair of waves
-constexpr int kKept = 32 * kWaves;                      // packed rows that a workgroup keeps
-template <int D>
-constexpr int stage_bytes() { return 2 * kTile * D * 2 + kTile * 8; }
+// Two sizes of a workgroup. Eight waves keep 128 keys and take the rows in
+// stages of 64; four keep 64 keys, take stages of 32 and leave room for a
+// second workgroup on the compute unit. The larger moves each row half as often
+// into LDS, the smaller fills the chip with short sequences (kManyGroups).
+constexpr int kTile = 64;                               // keys that pass by at a time (dq)
 constexpr int kPass = 64 * 4 * 16;                      // weights of 32 x 32 in fp32
-constexpr int kPassAll = kWaves / 2 * 2 * kPass;
-template <int D>
-constexpr int smem_bytes() { return 2 * stage_bytes<D>() + kPassAll; }
+template <int D, int W>
+struct Shape {
+  static constexpr int kKeys = 16 * W;                  // keys of a workgroup: 32 a pair of waves
+  static constexpr int kKept = 32 * W;                  // packed rows of a workgroup (dq)
+  static constexpr int kRows = 8 * W;                   // rows of a stage (dk, dv)
+  static constexpr int kBlocks = kRows / 32;
+  static constexpr int kStages = W == 8 ? 2 : 4;        // in LDS: one in use, the others on their way
+  static constexpr int kStage = 2 * kRows * D * 2 + kRows * 8;
+  static constexpr int kQStage = 2 * kTile * D * 2;
+  static constexpr int kKvBytes = kStages * kStage + W / 2 * kBlocks * kPass;
+  static constexpr int kBytes = kKvBytes > 2 * kQStage ? kKvBytes : 2 * kQStage;
+};
 
 // ---- dk, dv: a pair of waves keeps 32 keys (the lanes' columns), rows pass by ---
 // The first wave of a pair has the keys: scores, weights, dv = p^T do. The
@@ -101,25 +109,25 @@ constexpr int smem_bytes() { return 2 * stage_bytes<D>() + kPassAll; }
 // steps on the two tiles the other way round, and a wave's operands and sums
 // leave room for two waves a SIMD, of which one has products while the other
 // has elements.
-template <int D>
+template <int D, int W>
 __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int tile_index, uint8_t* smem) {
-  constexpr int RB = D * 2, S = D / 16, C = D / 32;
-  constexpr int kDo = kTile * RB;                       // dO's place behind Q's
-  constexpr int kStat = 2 * kTile * RB, kStage = stage_bytes<D>();
+  typedef Shape<D, W> Sh;
+  constexpr int RB = D * 2, S = D / 16, C = D / 32, R = Sh::kRows, kStage = Sh::kStage;
+  constexpr int kDo = R * RB, kStat = 2 * R * RB;       // places of dO and the statistics behind Q
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pair = wave & (kWaves / 2 - 1);
-  const bool has_keys = wave < kWaves / 2;
-  const SeqTile st = find_rows(p.cu_k, p.cu_q, p.B, p.Tk, p.Tq, 1, kKeys, tile_index);
+  const int pair = wave & (W / 2 - 1);
+  const bool has_keys = wave < W / 2;
+  const SeqTile st = find_rows(p.cu_k, p.cu_q, p.B, p.Tk, p.Tq, 1, Sh::kKeys, tile_index);
   if (st.b < 0) return;
   const int n_k = st.n;
   const int q_start = st.start2, n_q = st.n2, n_rows = n_q * p.g.d;
-  const int k0 = st.tile * kKeys;
+  const int k0 = st.tile * Sh::kKeys;
   const int key = k0 + pair * 32 + (lane & 31);
   const int keyc = key < n_k ? key : n_k - 1;
   const int shift = p.causal ? n_k - n_q : n_k;                // query i sees keys <= i + shift
   auto first_row = [&](int j) { return clamp_int(j - shift, 0, n_q) * p.g.d; };   // that sees key j
-  const int t_lo = first_row(k0) / kTile, t_hi = (n_rows + kTile - 1) / kTile;
+  const int t_lo = first_row(k0) / R, t_hi = (n_rows + R - 1) / R;
   // Row tiles are taken from the last one down, every parts-th: all workgroups
   // of a head, whose first rows differ, start with the same ones and meet them
   // in the XCD's L2.
@@ -129,25 +137,28 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
 
   const uint16_t* q = p.q + static_cast<int64_t>(q_start) * p.q_ld + head * p.g.d * D;
   const uint16_t* dout = p.dout + static_cast<int64_t>(q_start) * p.dout_ld + head * p.g.d * D;
-  const float2* stats = p.stats + static_cast<int64_t>(q_start) * p.nh + head * p.g.d;
-  float2 stat_next = make_float2(INFINITY, 0.f);
-  auto load = [&](int t, uint8_t* buf) {
-    rows_load<RB, kTile, kWaves>(q, p.q_ld, p.g, t * kTile, n_rows, buf, wave, lane);
-    rows_load<RB, kTile, kWaves>(dout, p.dout_ld, p.g, t * kTile, n_rows, buf + kDo, wave, lane);
+  // statistics of the group's rows: l2 of a stage's rows, then delta of them;
+  // behind the last row they are 0, as its q and dO are
+  const __amdgpu_buffer_rsrc_t stats =
+      buf_rsrc(p.stats + static_cast<int64_t>(q_start) * p.nh, static_cast<uint32_t>(n_q) * p.nh * 8u);
+  constexpr int kLoads = 2 * R * RB / 1024 / W;          // of a wave and stage, without the statistics
+  auto load = [&](int i) {
+    const int t = t_top - i * p.parts;
+    uint8_t* buf = smem + i % Sh::kStages * kStage;
+    rows_load<RB, R, W>(q, p.q_ld, p.g, t * R, n_rows, buf, wave, lane);
+    rows_load<RB, R, W>(dout, p.dout_ld, p.g, t * R, n_rows, buf + kDo, wave, lane);
     if (wave == 0) {
-      const int r = t * kTile + lane, tok = quot(r, p.g);
-      stat_next = r < n_rows ? stats[static_cast<int64_t>(tok) * p.nh + r - tok * p.g.d] : make_float2(INFINITY, 0.f);
+#pragma unroll
+      for (int x = 0; x < Sh::kBlocks; ++x) {
+        const int at = x * 64 + lane, r = t * R + (at & (R - 1)), tok = quot(r, p.g);
+        lds_load4_buf(stats, static_cast<uint32_t>(tok * p.nh + head * p.g.d + r - tok * p.g.d) * 8u + at / R * 4, 0,
+                      buf + kStat + x * 256);
+      }
     }
   };
-  // the statistics of 64 rows as two arrays, read as broadcasts of 4
-  auto put_stats = [&](uint8_t* buf) {
-    if (wave == 0) {
-      float* s = reinterpret_cast<float*>(buf + kStat);
-      s[lane] = stat_next.x;
-      s[64 + lane] = stat_next.y;
-    }
-  };
-  if (n_t > 0) load(t_top, smem);
+#pragma unroll
+  for (int i = 0; i + 1 < Sh::kStages; ++i)
+    if (i < n_t) load(i);
 
   bf16x8_t kept[S];
   {
@@ -164,7 +175,7 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int h = 0; h < 2; ++h) col_off[c][h] = col_operand_offset<RB>(lane, c, h) + (has_keys ? kDo : 0);
-  f32x4_t* pass = reinterpret_cast<f32x4_t*>(smem + 2 * kStage + pair * 2 * kPass) + lane;
+  f32x4_t* pass = reinterpret_cast<f32x4_t*>(smem + Sh::kStages * kStage + pair * Sh::kBlocks * kPass) + lane;
   f32x16_t sum[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) sum[c] = f32x16_t{};
@@ -173,21 +184,25 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   auto tile = [&](int i, auto cut_c) __attribute__((always_inline)) {
     constexpr bool kCut = decltype(cut_c)::value;
     const int t = t_top - i * p.parts;
-    uint8_t* buf = smem + (i & 1) * kStage;
-    put_stats(buf);                   // the other buffer's readers are a barrier behind
-    wait_vmcnt<0>();
+    const uint8_t* buf = smem + i % Sh::kStages * kStage;
+    // this stage is in place; those behind it may be on their way
+    const int ahead = min(Sh::kStages - 2, n_t - 1 - i);
+    constexpr int kMine = kLoads + Sh::kBlocks;         // of the wave that loads the statistics
+    if (ahead <= 0) wait_vmcnt<0>();
+    else if (ahead == 1) wave == 0 ? wait_vmcnt<kMine>() : wait_vmcnt<kLoads>();
+    else wave == 0 ? wait_vmcnt<2 * kMine>() : wait_vmcnt<2 * kLoads>();
     lds_barrier();
-    if (i + 1 < n_t) load(t - p.parts, smem + ((i + 1) & 1) * kStage);
+    if (i + Sh::kStages - 1 < n_t) load(i + Sh::kStages - 1);
     const float* stat = reinterpret_cast<const float*>(buf + kStat) + 4 * g;
-    f32x16_t x[2];
+    f32x16_t x[Sh::kBlocks];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < Sh::kBlocks; ++b)
 #pragma unroll
       for (int k = 0; k < S; ++k)
         x[b] = mfma(row_operand(buf, row_off[k] + b * 32 * RB), kept[k], k == 0 ? f32x16_t{} : x[b]);
     if (has_keys) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < Sh::kBlocks; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const f32x4_t l2 = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j);
@@ -195,7 +210,7 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             w[e] = exp2_hw(fmaf(x[b][4 * j + e], c2, -l2[e]));
-            if constexpr (kCut) w[e] = t * kTile + 32 * b + 8 * j + 4 * g + e < row_min ? 0.f : w[e];
+            if constexpr (kCut) w[e] = t * R + 32 * b + 8 * j + 4 * g + e < row_min ? 0.f : w[e];
             x[b][4 * j + e] = w[e];
           }
           pass[(4 * b + j) * 64] = w;
@@ -204,17 +219,17 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
     } else {
       lds_barrier();
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < Sh::kBlocks; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(stat + 64 + 32 * b + 8 * j);
+          const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(stat + R + 32 * b + 8 * j);
           const f32x4_t w = pass[(4 * b + j) * 64];
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[b][4 * j + e] = w[e] * (x[b][4 * j + e] - delta[e]);
         }
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < Sh::kBlocks; ++b)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const bf16x8_t f = pack_operand(x[b], k);
@@ -225,7 +240,7 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
       }
   };
   // the tiles that the causal mask cuts come last
-  const int cut_hi = p.causal ? (first_row(min(k0 + kKeys, n_k) - 1) + kTile - 1) / kTile : 0;
+  const int cut_hi = p.causal ? (first_row(min(k0 + Sh::kKeys, n_k) - 1) + R - 1) / R : 0;
   const int n_whole = t_top >= cut_hi ? min(n_t, (t_top - cut_hi) / p.parts + 1) : 0;
   int i = 0;
   for (; i < n_whole; ++i) tile(i, std::false_type{});
@@ -234,7 +249,7 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   lds_barrier();                        // everyone is done with the tiles
   const int64_t tok = static_cast<int64_t>(st.start) + k0 + pair * 32;
   const int n_out = n_k - k0 - pair * 32;
-  static_assert(kWaves * result_bytes<RB>() <= smem_bytes<D>(), "results fit the tile buffers");
+  static_assert(W * result_bytes<RB>() <= Sh::kBytes, "results fit the tile buffers");
   if (p.parts == 1) {
     uint8_t* rows = smem + wave * result_bytes<RB>();
     const float sc = has_keys ? 1.f : p.scale;
@@ -259,11 +274,11 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
 }
 
 // ---- dq: a wave keeps 32 packed rows (the lanes' columns), keys pass by --------
-template <int D>
+template <int D, int W>
 __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index, uint8_t* smem) {
   constexpr int RB = D * 2, S = D / 16, C = D / 32;
   constexpr int kV = kTile * RB;                        // V's place behind K's
-  constexpr int kStage = stage_bytes<D>();
+  constexpr int kStage = Shape<D, W>::kQStage, kKept = Shape<D, W>::kKept;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const SeqTile st = find_rows(p.cu_q, p.cu_k, p.B, p.Tq, p.Tk, p.g.d, kKept, tile_index);
@@ -288,9 +303,9 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
   auto load = [&](int kt, uint8_t* buf) {
     const int n = n_k - kt * kTile;
     const int nv = n < kTile ? n : kTile;
-    tile_load<RB, kTile, kWaves>(kb + static_cast<int64_t>(kt) * kTile * p.k_ld, static_cast<uint32_t>(p.k_ld * 2), nv,
+    tile_load<RB, kTile, W>(kb + static_cast<int64_t>(kt) * kTile * p.k_ld, static_cast<uint32_t>(p.k_ld * 2), nv,
                                  buf, wave, lane);
-    tile_load<RB, kTile, kWaves>(vb + static_cast<int64_t>(kt) * kTile * p.v_ld, static_cast<uint32_t>(p.v_ld * 2), nv,
+    tile_load<RB, kTile, W>(vb + static_cast<int64_t>(kt) * kTile * p.v_ld, static_cast<uint32_t>(p.v_ld * 2), nv,
                                  buf + kV, wave, lane);
   };
   if (n_kt > 0) load(0, smem);
@@ -371,18 +386,18 @@ __device__ __forceinline__ void bwd_q(const BwdArgs& p, int head, int tile_index
 // chip. The kind whose workgroups walk more tiles comes first. Heads run
 // fastest (an XCD keeps to its own where their number is a multiple of 8); the
 // tiles that see most come first.
-template <int D>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
+template <int D, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void bwd_kernel(BwdArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[smem_bytes<D>()];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Shape<D, W>::kBytes];
   const int n_kv = p.k_tiles * p.nkv * p.parts, n_q = p.q_tiles * p.nkv;
   const int id = blockIdx.x;
   const int head = id % p.nkv;
   if (p.q_first ? id >= n_q : id < n_kv) {
     const int r = (p.q_first ? id - n_q : id) / p.nkv;
-    bwd_kv<D>(p, head, r % p.parts, r / p.parts, smem);
+    bwd_kv<D, W>(p, head, r % p.parts, r / p.parts, smem);
   } else {
-    bwd_q<D>(p, head, p.q_tiles - 1 - (p.q_first ? id : id - n_kv) / p.nkv, smem);
+    bwd_q<D, W>(p, head, p.q_tiles - 1 - (p.q_first ? id : id - n_kv) / p.nkv, smem);
   }
 }
 
@@ -413,12 +428,21 @@ __global__ __launch_bounds__(256) void bwd_join_kernel(BwdArgs p) {
     *reinterpret_cast<uint2*>(p.dv + t * p.dv_ld + head * D + c - D) = pack4(s[0], s[1], s[2], s[3]);
 }
 
+// Eight waves a workgroup where there are many rows (tokens x heads) and long
+// sequences. Forward and backward in us, eight / four waves, 128 values a head:
+// 4096 tokens in 2 sequences x 64 heads 723 / 863, 1500 x 64 220 / 269, 4 x 600 x
+// 64 213 / 237, 4000 x 32 620 / 722; but 2048 x 16 150 / 136, 512 x 128 106 / 83,
+// 8 x 300 x 64 156 / 142, 3 x 1000 x 8 99 / 82.
+constexpr int kManyRows = 1 << 16, kLong = 576;
+int waves_of(int B, int Tq, int Tk, int nh) {
+  return static_cast<int64_t>(Tq) * nh >= kManyRows && Tk / B >= kLong ? 8 : 4;
+}
 // Parts that the rows of a key tile are cut into: enough workgroups for two a
-// compute unit, as far as a part keeps 4 tiles of rows in the mean.
+// compute unit, as far as a part keeps 4 stages of rows in the mean.
 constexpr int kMaxParts = 32;
-int parts_of(int Tq, int Tk, int nh, int nkv) {
-  const int64_t wgs = (static_cast<int64_t>(Tk) + kKeys - 1) / kKeys * nkv;
-  const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (4 * kTile);
+int parts_of(int w, int Tq, int Tk, int nh, int nkv) {
+  const int64_t wgs = (static_cast<int64_t>(Tk) + 16 * w - 1) / (16 * w) * nkv;
+  const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (32 * w);
   int64_t n = 2 * kNumCu / (wgs > 0 ? wgs : 1);
   n = n < tiles ? n : tiles;
   return n < 1 ? 1 : (n > kMaxParts ? kMaxParts : static_cast<int>(n));
@@ -426,21 +450,24 @@ int parts_of(int Tq, int Tk, int nh, int nkv) {
 // Rows of the parts' sums: parts_of never brings them above either bound, and
 // both grow with the sizes, so a workspace serves every smaller call.
 size_t part_rows(int Tk, int nkv) {
-  const size_t all = size_t{kMaxParts} * Tk * nkv, most = size_t{2} * kNumCu * kKeys;
+  const size_t all = size_t{kMaxParts} * Tk * nkv, most = size_t{2} * kNumCu * 128;
   return all < most ? all : most;
 }
 size_t stats_bytes(int Tq, int nh) { return (static_cast<size_t>(Tq) * nh * 8 + 255) & ~size_t{255}; }
 
 template <int D>
-void launch_bwd(const BwdArgs& a, hipStream_t stream) {
+void launch_bwd(BwdArgs a, int waves, hipStream_t stream) {
   if (a.Tq > 0) {
     const int64_t rows = static_cast<int64_t>(a.Tq) * a.nh;
     constexpr int kPer = 256 / (D / 8);
     hipLaunchKernelGGL(bwd_stats_kernel<D>, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)), dim3(256), 0, stream,
                        a);
   }
-  hipLaunchKernelGGL(bwd_kernel<D>, dim3(static_cast<unsigned>(a.k_tiles * a.parts + a.q_tiles) * a.nkv),
-                     dim3(64 * kWaves), 0, stream, a);
+  a.k_tiles = a.Tk > 0 ? a.Tk / (16 * waves) + (a.B < a.Tk ? a.B : a.Tk) : 0;
+  a.q_tiles = a.Tq > 0 ? a.Tq * a.g.d / (32 * waves) + (a.B < a.Tq ? a.B : a.Tq) : 0;
+  const dim3 grid(static_cast<unsigned>(a.k_tiles * a.parts + a.q_tiles) * a.nkv);
+  if (waves == 8) hipLaunchKernelGGL((bwd_kernel<D, 8>), grid, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((bwd_kernel<D, 4>), grid, dim3(256), 0, stream, a);
   if (a.parts > 1) {
     constexpr int kPer = 256 / (D / 2);
     const int64_t units = static_cast<int64_t>(a.Tk) * a.nkv;
@@ -501,11 +528,10 @@ extern "C" int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q
   a.dv = static_cast<uint16_t*>(dv), a.dv_ld = dv_ld;
   a.stats = static_cast<float2*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + stats_bytes(Tq, n_heads));
-  a.parts = parts_of(Tq, Tk, n_heads, n_kv_heads);
-  a.k_tiles = Tk > 0 ? Tk / kKeys + (B < Tk ? B : Tk) : 0;
-  a.q_tiles = Tq > 0 ? Tq * a.g.d / kKept + (B < Tq ? B : Tq) : 0;
+  const int waves = waves_of(B, Tq, Tk, n_heads);
+  a.parts = parts_of(waves, Tq, Tk, n_heads, n_kv_heads);
   a.q_first = static_cast<int64_t>(Tq) * a.g.d / a.parts < Tk;
-  if (head_dim == 128) launch_bwd<128>(a, stream);
-  else launch_bwd<64>(a, stream);
+  if (head_dim == 128) launch_bwd<128>(a, waves, stream);
+  else launch_bwd<64>(a, waves, stream);
   return check_launch(fn);
 }

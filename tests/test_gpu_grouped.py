@@ -179,6 +179,10 @@ PACKED = [
     (8, 2, 64, [3, 20], [1500, 700], True),           # the forward's keys in parts
     (2, 1, 128, [1, 5, 2], [2100, 0, 3], False),      # parts without keys
     (12, 4, 128, [40, 7], [900, 600], False),
+    # many rows of long sequences: the backward's larger workgroups
+    (512, 16, 128, [129], [600], True),
+    (256, 8, 64, [200, 0, 57], [1500, 9, 300], False),
+    (110, 22, 64, [597, 3], [1197, 3], True),
 ]
 
 
