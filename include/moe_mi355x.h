@@ -23,7 +23,9 @@
  * the routed and the shared expert in the same launches). The backward of
  * the routed experts is moe_grouped_mlp_bwd. The attention beside it is
  * moe_mla_attn_fwd / moe_mla_attn_bwd (prompts, training) and moe_mla_append
- * -> moe_mla_decode (serving over a paged latent cache).
+ * -> moe_mla_decode (serving over a paged latent cache), or with grouped heads
+ * moe_qk_norm_rope, moe_gqa_attn_fwd / moe_gqa_attn_bwd and moe_gqa_append ->
+ * moe_gqa_decode (serving over a paged 8-bit cache).
  *
  * Conventions for every call
  *   - Pointers are device pointers owned by the caller unless stated; the
@@ -868,6 +870,8 @@ size_t moe_gqa_attn_fwd_workspace(int Tq, int n_heads, int head_dim);
  * A query without keys gives out 0 and lse -inf. A key that is hidden from
  * some queries of its sequence and shown to others must have a finite value
  * row: its weight 0 still multiplies it, as in the formula's matrix product.
+ * ws       moe_gqa_attn_fwd_workspace(Tq, n_heads, head_dim) bytes, of any
+ *          content; calls that may run at the same time need one each.
  * Limits: Tq * n_heads and Tk * n_heads <= 2^27, B * n_heads <= 2^22. Tq == 0
  * or B == 0 is a no-op.
  */
@@ -926,8 +930,8 @@ int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q
  * ones) are rounded again under it (they keep their digits down to the codes'
  * smallest normal number, 2^-6 of the scale). Bytes of later positions are not
  * changed. So a token gives the same codes in whichever pieces its request
- * arrives, up to that second rounding. Two requests of a call must not write
- * to the same block.
+ * arrives, up to that second rounding. The blocks that a call writes must be
+ * different ones: no page twice among them, of one request or of two.
  * k, v     [T, n_kv_heads, head_dim] bf16, rows k_ld, v_ld apart. Values are
  *          expected to be finite and below 2^127: NaN and infinities become
  *          NaN codes, and an infinity brings its block to the largest scale.

@@ -1,5 +1,5 @@
-// Device helpers shared by the latent-attention kernels: sizes, LDS tile
-// layouts and their loaders, matrix-core operand reads, packed sequences.
+// Device helpers shared by the attention kernels: latent attention's sizes, LDS
+// tile layouts and their loaders, matrix-core operand reads, packed sequences.
 //
 // Latent attention keeps one latent vector c (512 values) and one rotary key
 // (64 values) per token for all heads; head h's key is (W_UK[h] c | rotary

@@ -77,7 +77,8 @@ class QKNormRope:
     many of a head's first values are turned (a multiple of 16; default: all);
     interleaved: pairs (2 i, 2 i + 1) instead of (i, i + rotary / 2). Outputs
     are views of the object's buffers, as many rows as the call's inputs have;
-    backward=True adds the gradients' buffers and workspace."""
+    backward=True adds the gradients' buffers and workspace. One object's calls
+    must not overlap."""
 
     def __init__(self, *, T, n_heads, n_kv_heads, head_dim=128, rotary=None, interleaved=False, eps=1e-6,
                  backward=False, device="cuda"):
@@ -262,7 +263,7 @@ def _requests(cache, page_table, lens, cu, dev):
 def grouped_cache_append(k, v, cache, page_table, lens, cu, stream=None):
     """New keys and values (rotated already) [T, n_kv_heads, head_dim] bf16
     into the cache: request b's rows cu[b] .. cu[b + 1] become its last tokens,
-    lens[b] (new ones included) counts them. page_table [B, max_pages] int32,
+    lens[b] (new ones included) counts them. The pages written are distinct. page_table [B, max_pages] int32,
     lens [B] and cu [B + 1] int32."""
     T, kv, d = k.shape[0], cache.n_kv_heads, cache.head_dim
     if v.shape[0] != T:
@@ -275,13 +276,16 @@ def grouped_cache_append(k, v, cache, page_table, lens, cu, stream=None):
 
 class GroupedDecode:
     """Attention over a GroupedCache for up to max_tokens new tokens of up to
-    max_seqs requests a call. scale defaults to head_dim ** -0.5."""
+    max_seqs requests a call. scale defaults to head_dim ** -0.5. One object's
+    calls must not overlap; it is built outside of a graph's capture."""
 
     def __init__(self, *, n_heads, n_kv_heads, head_dim=128, max_tokens, max_seqs, scale=None, device="cuda"):
         _heads(n_heads, n_kv_heads, head_dim)
         if not (1 <= max_seqs <= 65536 and max_seqs * n_kv_heads <= 1 << 19 and 1 <= max_tokens and
                 max_tokens * n_heads <= 1 << 24):
             raise ValueError("moe_gqa_decode does not support these sizes")
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise ValueError("GroupedDecode clears its workspace once, so it cannot be built during a capture")
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
         self.max_tokens, self.max_seqs = max_tokens, max_seqs
         self.scale = head_dim ** -0.5 if scale is None else scale

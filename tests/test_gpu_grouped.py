@@ -750,3 +750,37 @@ def test_class_refusals(gpu_lib):
             n(q, k, **kw)
     with pytest.raises(ValueError):
         n(q, k[:3])
+
+
+def test_no_decode_object_during_a_capture(gpu_lib):
+    """Its workspace is cleared once, which a capture would only record."""
+    g = torch.cuda.CUDAGraph()
+    x = torch.zeros(4, device="cuda")
+    with torch.cuda.graph(g):
+        x.add_(1)
+        with pytest.raises(ValueError):
+            moe.GroupedDecode(n_heads=4, n_kv_heads=2, head_dim=64, max_tokens=2, max_seqs=1)
+    g.replay()
+    torch.cuda.synchronize()
+    assert (x == 1).all()
+
+
+def test_layer_example(gpu_lib):
+    """The example layer: prompt, decode steps, a drafted tree, gradients."""
+    log("grouped layer example")
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "grouped_moe_layer.py")
+    spec = importlib.util.spec_from_file_location("grouped_moe_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    worst, tree, grads, y = mod.main(heads=16, kv_heads=2, hidden=512, prompt=130, steps=3)
+    torch.cuda.synchronize()
+    # a code is off by at most 2^-4 of its value, evenly spread (1 / sqrt(3) of
+    # that in the mean square). Values carry it to the output as it is; keys to
+    # scores of variance 1 and so to the weights, relatively. The two together
+    # 0.051 of the output's norm, twice that for one short draw.
+    assert worst < 2 * 2 ** 0.5 * 2.0 ** -4 / 3 ** 0.5
+    # the same codes in other places: weights and result rounded on each side
+    assert tree < 4 * 2.0 ** -8
+    assert all(torch.isfinite(t.float()).all() for t in grads) and torch.isfinite(y.float()).all()
