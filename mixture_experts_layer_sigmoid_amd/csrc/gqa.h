@@ -99,6 +99,34 @@ __device__ __forceinline__ void rows_load(const uint16_t* base, int64_t ld, cons
   }
 }
 
+// The same for tiles that follow one another where the group divides the rows
+// that the waves load at a time: a tile is whole tokens and all tiles' offsets
+// are the first one's, so that nothing is left to compute per lane and tile
+// (backward of 4096 tokens x 64 heads 1 to 2%).
+template <int RB, int ROWS, int NW>
+struct EvenRows {
+  static constexpr int kPer = 1024 / RB, kStep = kPer * NW;
+  const uint16_t* base;
+  int64_t ld;
+  uint32_t ld_b, off, step;
+  int n_q, per;                                          // tokens of the sequence and of a tile
+
+  static __device__ __forceinline__ bool fits(const Div& g) { return kStep % g.d == 0; }
+  __device__ __forceinline__ EvenRows(const uint16_t* b, int64_t l, const Div& g, int n, int wave, int lane)
+      : base(b), ld(l), ld_b(static_cast<uint32_t>(l * 2)), n_q(n), per(ROWS / g.d) {
+    const int c = lane & (RB / 16 - 1), r = wave * kPer + lane / (RB / 16), t = quot(r, g);
+    off = static_cast<uint32_t>(t) * ld_b + static_cast<uint32_t>(r - t * g.d) * RB + ((c ^ tile_key<RB>(r)) << 4);
+    step = static_cast<uint32_t>(kStep / g.d) * ld_b;
+  }
+  __device__ __forceinline__ void load(int tile, const Div& g, uint8_t* lds, int wave) const {
+    const int t0 = tile * per;
+    const uint32_t bytes = static_cast<uint32_t>(min(per, n_q - t0) - 1) * ld_b + g.d * RB;
+    const __amdgpu_buffer_rsrc_t rs = buf_rsrc(base + static_cast<int64_t>(t0) * ld, bytes);
+#pragma unroll
+    for (int i = 0; i < ROWS / kStep; ++i) lds_load16_buf(rs, off + i * step, 0, lds + (wave + i * NW) * 1024);
+  }
+};
+
 // A wave's 32 result rows (packed rows r0 .. of one key head) from LDS to
 // memory; dst: the sequence's first token at the group's first head.
 template <int RB>

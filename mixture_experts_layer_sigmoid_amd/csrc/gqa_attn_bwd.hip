@@ -101,10 +101,14 @@ struct Shape {
   static constexpr int kKept = 32 * W;                  // packed rows of a workgroup (dq)
   static constexpr int kRows = 8 * W;                   // rows of a stage (dk, dv)
   static constexpr int kBlocks = kRows / 32;
-  static constexpr int kStages = W == 8 ? 2 : 4;        // in LDS: one in use, the others on their way
-  static constexpr int kStage = 2 * kRows * D * 2 + kRows * 8;
+  // stages in LDS: of dO the one in use and those on their way; Q and the
+  // statistics stay one stage longer
+  static constexpr int kDoStages = W == 8 ? 2 : 3, kQStages = kDoStages + 1;
+  static constexpr int kDoBytes = kRows * D * 2, kQBytes = kDoBytes + kRows * 8;
+  static constexpr int kQPlace = kDoStages * kDoBytes, kPassPlace = kQPlace + kQStages * kQBytes;
+  static constexpr int kPassBytes = W / 2 * kBlocks * kPass;
+  static constexpr int kKvBytes = kPassPlace + 2 * kPassBytes;
   static constexpr int kQStage = 2 * kTile * D * 2;
-  static constexpr int kKvBytes = kStages * kStage + W / 2 * kBlocks * kPass;
   static constexpr int kBytes = kKvBytes > 2 * kQStage ? kKvBytes : 2 * kQStage;
 };
 
@@ -113,13 +117,15 @@ struct Shape {
 // second has their values: dp, ds with the weights that the first left in LDS
 // (fp32, as they lie in its accumulator), dk = ds^T q. So both take the same
 // steps on the two tiles the other way round, and a wave's operands and sums
-// leave room for two waves a SIMD, of which one has products while the other
-// has elements.
+// leave room for two waves a SIMD. The second wave is a stage behind the first
+// with ds and dk: between two barriers neither waits for the other, and its
+// products fill the time of the first one's exponentials (forward and backward
+// of 8 x 300 tokens x 64 heads 140 -> 127 us, 2 x 2000 x 16 234 -> 222, with eight
+// waves no change).
 template <int D, int W>
 __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int tile_index, uint8_t* smem) {
   typedef Shape<D, W> Sh;
-  constexpr int RB = D * 2, S = D / 16, C = D / 32, R = Sh::kRows, kStage = Sh::kStage;
-  constexpr int kDo = R * RB, kStat = 2 * R * RB;       // places of dO and the statistics behind Q
+  constexpr int RB = D * 2, S = D / 16, C = D / 32, R = Sh::kRows;
   const int lane = threadIdx.x & 63, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pair = wave & (W / 2 - 1);
@@ -148,22 +154,31 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
   const __amdgpu_buffer_rsrc_t stats =
       buf_rsrc(p.stats + static_cast<int64_t>(q_start) * p.nh, static_cast<uint32_t>(n_q) * p.nh * 8u);
   constexpr int kLoads = 2 * R * RB / 1024 / W;          // of a wave and stage, without the statistics
+  auto do_at = [&](int i) { return smem + i % Sh::kDoStages * Sh::kDoBytes; };
+  auto q_at = [&](int i) { return smem + Sh::kQPlace + i % Sh::kQStages * Sh::kQBytes; };
+  typedef EvenRows<RB, R, W> Rows;
+  const bool even = Rows::fits(p.g);
+  const Rows q_rows(q, p.q_ld, p.g, n_q, wave, lane), do_rows(dout, p.dout_ld, p.g, n_q, wave, lane);
   auto load = [&](int i) {
     const int t = t_top - i * p.parts;
-    uint8_t* buf = smem + i % Sh::kStages * kStage;
-    rows_load<RB, R, W>(q, p.q_ld, p.g, t * R, n_rows, buf, wave, lane);
-    rows_load<RB, R, W>(dout, p.dout_ld, p.g, t * R, n_rows, buf + kDo, wave, lane);
+    if (even) {
+      q_rows.load(t, p.g, q_at(i), wave);
+      do_rows.load(t, p.g, do_at(i), wave);
+    } else {
+      rows_load<RB, R, W>(q, p.q_ld, p.g, t * R, n_rows, q_at(i), wave, lane);
+      rows_load<RB, R, W>(dout, p.dout_ld, p.g, t * R, n_rows, do_at(i), wave, lane);
+    }
     if (wave == 0) {
 #pragma unroll
       for (int x = 0; x < Sh::kBlocks; ++x) {
         const int at = x * 64 + lane, r = t * R + (at & (R - 1)), tok = quot(r, p.g);
         lds_load4_buf(stats, static_cast<uint32_t>(tok * p.nh + head * p.g.d + r - tok * p.g.d) * 8u + at / R * 4, 0,
-                      buf + kStat + x * 256);
+                      q_at(i) + Sh::kDoBytes + x * 256);
       }
     }
   };
 #pragma unroll
-  for (int i = 0; i + 1 < Sh::kStages; ++i)
+  for (int i = 0; i + 1 < Sh::kDoStages; ++i)
     if (i < n_t) load(i);
 
   bf16x8_t kept[S];
@@ -173,67 +188,42 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
 #pragma unroll
     for (int s = 0; s < S; ++s) kept[s] = *reinterpret_cast<const bf16x8_t*>(x + 16 * s);
   }
-  // rows of Q or dO as they lie, columns of the other tile
+  // rows of one tile as they lie, columns of the other
   uint32_t row_off[S], col_off[C][2];
 #pragma unroll
-  for (int s = 0; s < S; ++s) row_off[s] = row_operand_offset<RB>(lane, s) + (has_keys ? 0 : kDo);
+  for (int s = 0; s < S; ++s) row_off[s] = row_operand_offset<RB>(lane, s);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) col_off[c][h] = col_operand_offset<RB>(lane, c, h) + (has_keys ? kDo : 0);
-  f32x4_t* pass = reinterpret_cast<f32x4_t*>(smem + Sh::kStages * kStage + pair * Sh::kBlocks * kPass) + lane;
-  f32x16_t sum[C];
+    for (int h = 0; h < 2; ++h) col_off[c][h] = col_operand_offset<RB>(lane, c, h);
+  auto pass_at = [&](int i) {
+    return reinterpret_cast<f32x4_t*>(smem + Sh::kPassPlace + (i & 1) * Sh::kPassBytes + pair * Sh::kBlocks * kPass) +
+           lane;
+  };
+  f32x16_t sum[C], x[Sh::kBlocks];
 #pragma unroll
   for (int c = 0; c < C; ++c) sum[c] = f32x16_t{};
-  const float c2 = p.scale * kLog2e;
 
-  auto tile = [&](int i, auto cut_c) __attribute__((always_inline)) {
-    constexpr bool kCut = decltype(cut_c)::value;
-    const int t = t_top - i * p.parts;
-    const uint8_t* buf = smem + i % Sh::kStages * kStage;
-    // this stage is in place; those behind it may be on their way
-    const int ahead = min(Sh::kStages - 2, n_t - 1 - i);
-    constexpr int kMine = kLoads + Sh::kBlocks;         // of the wave that loads the statistics
-    if (ahead <= 0) wait_vmcnt<0>();
-    else if (ahead == 1) wave == 0 ? wait_vmcnt<kMine>() : wait_vmcnt<kLoads>();
-    else wave == 0 ? wait_vmcnt<2 * kMine>() : wait_vmcnt<2 * kLoads>();
+  // Stage i is in place (those behind it may be on their way), all waves are
+  // done with their last step, and the next stage is asked for.
+  auto next = [&](int i) __attribute__((always_inline)) {
+    if (i < n_t) {
+      const int ahead = min(Sh::kDoStages - 2, n_t - 1 - i);
+      if (ahead <= 0) wait_vmcnt<0>();
+      else wave == 0 ? wait_vmcnt<kLoads + Sh::kBlocks>() : wait_vmcnt<kLoads>();
+    }
+    static_assert(Sh::kDoStages <= 3, "at most one stage behind");
     lds_barrier();
-    if (i + Sh::kStages - 1 < n_t) load(i + Sh::kStages - 1);
-    const float* stat = reinterpret_cast<const float*>(buf + kStat) + 4 * g;
-    f32x16_t x[Sh::kBlocks];
+    if (i + Sh::kDoStages - 1 < n_t) load(i + Sh::kDoStages - 1);
+  };
+  auto rows_product = [&](const uint8_t* buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < Sh::kBlocks; ++b)
 #pragma unroll
       for (int k = 0; k < S; ++k)
         x[b] = mfma(row_operand(buf, row_off[k] + b * 32 * RB), kept[k], k == 0 ? f32x16_t{} : x[b]);
-    if (has_keys) {
-#pragma unroll
-      for (int b = 0; b < Sh::kBlocks; ++b)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x4_t l2 = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j);
-          f32x4_t w;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] = exp2_hw(fmaf(x[b][4 * j + e], c2, -l2[e]));
-            if constexpr (kCut) w[e] = t * R + 32 * b + 8 * j + 4 * g + e < row_min ? 0.f : w[e];
-            x[b][4 * j + e] = w[e];
-          }
-          pass[(4 * b + j) * 64] = w;
-        }
-      lds_barrier();
-    } else {
-      lds_barrier();
-#pragma unroll
-      for (int b = 0; b < Sh::kBlocks; ++b)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(stat + R + 32 * b + 8 * j);
-          const f32x4_t w = pass[(4 * b + j) * 64];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[b][4 * j + e] = w[e] * (x[b][4 * j + e] - delta[e]);
-        }
-    }
+  };
+  auto add_columns = [&](const uint8_t* buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < Sh::kBlocks; ++b)
 #pragma unroll
@@ -245,12 +235,58 @@ __device__ __forceinline__ void bwd_kv(const BwdArgs& p, int head, int part, int
                         f, sum[c]);
       }
   };
-  // the tiles that the causal mask cuts come last
-  const int cut_hi = p.causal ? (first_row(min(k0 + Sh::kKeys, n_k) - 1) + R - 1) / R : 0;
-  const int n_whole = t_top >= cut_hi ? min(n_t, (t_top - cut_hi) / p.parts + 1) : 0;
-  int i = 0;
-  for (; i < n_whole; ++i) tile(i, std::false_type{});
-  for (; i < n_t; ++i) tile(i, std::true_type{});
+  if (has_keys) {
+    const float c2 = p.scale * kLog2e;
+    auto step = [&](int i, auto cut_c) __attribute__((always_inline)) {
+      constexpr bool kCut = decltype(cut_c)::value;
+      next(i);
+      rows_product(q_at(i));
+      const float* stat = reinterpret_cast<const float*>(q_at(i) + Sh::kDoBytes) + 4 * g;
+      f32x4_t* pass = pass_at(i);
+      const int r0 = (t_top - i * p.parts) * R + 4 * g;
+#pragma unroll
+      for (int b = 0; b < Sh::kBlocks; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4_t l2 = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j);
+          f32x4_t w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = exp2_hw(fmaf(x[b][4 * j + e], c2, -l2[e]));
+            if constexpr (kCut) w[e] = r0 + 32 * b + 8 * j + e < row_min ? 0.f : w[e];
+            x[b][4 * j + e] = w[e];
+          }
+          pass[(4 * b + j) * 64] = w;
+        }
+      add_columns(do_at(i));
+    };
+    // the tiles that the causal mask cuts come last
+    const int cut_hi = p.causal ? (first_row(min(k0 + Sh::kKeys, n_k) - 1) + R - 1) / R : 0;
+    const int n_whole = t_top >= cut_hi ? min(n_t, (t_top - cut_hi) / p.parts + 1) : 0;
+    int i = 0;
+    for (; i < n_whole; ++i) step(i, std::false_type{});
+    for (; i < n_t; ++i) step(i, std::true_type{});
+    next(n_t);
+  } else {
+    for (int i = 0; i <= n_t; ++i) {
+      next(i);
+      if (i > 0) {
+        const float* stat = reinterpret_cast<const float*>(q_at(i - 1) + Sh::kDoBytes) + R + 4 * g;
+        const f32x4_t* pass = pass_at(i - 1);
+#pragma unroll
+        for (int b = 0; b < Sh::kBlocks; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(stat + 32 * b + 8 * j);
+            const f32x4_t w = pass[(4 * b + j) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[b][4 * j + e] = w[e] * (x[b][4 * j + e] - delta[e]);
+          }
+        add_columns(q_at(i - 1));
+      }
+      if (i < n_t) rows_product(do_at(i));
+    }
+  }
 
   lds_barrier();                        // everyone is done with the tiles
   const int64_t tok = static_cast<int64_t>(st.start) + k0 + pair * 32;
@@ -436,10 +472,10 @@ __global__ __launch_bounds__(256) void bwd_join_kernel(BwdArgs p) {
 
 // Eight waves a workgroup where there are many rows (tokens x heads) and long
 // sequences. Forward and backward in us, eight / four waves, 128 values a head:
-// 4096 tokens in 2 sequences x 64 heads 723 / 863, 1500 x 64 220 / 269, 4 x 600 x
-// 64 213 / 237, 4000 x 32 620 / 722; but 2048 x 16 150 / 136, 512 x 128 106 / 83,
-// 8 x 300 x 64 156 / 142, 3 x 1000 x 8 99 / 82.
-constexpr int kManyRows = 1 << 16, kLong = 576;
+// 4096 tokens in 2 sequences x 64 heads 725 / 768, 3500 in 2 x 32 287 / 321, 1500
+// x 64 228 / 246; but 4096 x 16 400 / 363, 5 x 800 x 64 351 / 323, 8 x 300 x 64
+// 155 / 129, 512 x 128 111 / 84.
+constexpr int kManyRows = 90000, kLong = 1200;
 int waves_of(int B, int Tq, int Tk, int nh) {
   return static_cast<int64_t>(Tq) * nh >= kManyRows && Tk / B >= kLong ? 8 : 4;
 }

@@ -183,6 +183,9 @@ PACKED = [
     (512, 16, 128, [129], [600], True),
     (256, 8, 64, [200, 0, 57], [1500, 9, 300], False),
     (110, 22, 64, [597, 3], [1197, 3], True),
+    (704, 22, 128, [129], [1201], True),
+    (512, 8, 64, [130, 0, 57], [2500, 1109, 0], False),
+    (360, 72, 128, [251], [1250], True),
 ]
 
 
