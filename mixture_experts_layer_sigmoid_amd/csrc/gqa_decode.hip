@@ -99,9 +99,16 @@ __device__ __forceinline__ int piece_tiles(const DecodeArgs& p, int64_t all, int
   }
   // requests whose rows overlap can exceed the grid: then nothing is cut
   if (segs > p.segs) return 1 << 30;
-  // two workgroups fill a compute unit: while the segments leave room, all
-  // pieces run at once
-  const int64_t n = segs >= kPieces ? kPieces : (segs > kPieces / 2 ? kPieces / 2 : kPieces - segs);
+  // A segment's last piece is half a piece on average, so there are about n +
+  // segs / 2 of them. Few segments: one piece a compute unit (a second does not
+  // read faster, and is joined: 8 long caches 38 us, two a unit 41; 8 requests
+  // with 8 new tokens 23.3 and 26). Some segments: as many as two a unit hold at
+  // once (20 of up to 8000 tokens 44.6 us, one a unit 46). Many: shorter pieces
+  // the more segments there are, so that the last to end are short (48 of up to
+  // 8000 tokens n = 256 98 us, 320 107; 64 of them 106, n = 512 113; 100 of them
+  // n = 512 175, 256 184).
+  const int64_t n = segs <= kNumCu / 2 ? kNumCu - segs / 2 : segs <= kNumCu ? kPieces - segs
+                    : segs < 3 * kNumCu ? kPieces / 2 : kPieces;
   const int64_t c = (all + n - 1) / n;
   return c > kLeast ? static_cast<int>(c < (1 << 30) ? c : (1 << 30)) : kLeast;
 }
