@@ -20,11 +20,11 @@
 // Codes times scales are exact in bf16; scores and all sums are fp32.
 //
 // Memory bounds long caches: 64 requests of 176k tokens x 8 key heads of 128
-// take 88 us (4.2 TB/s of 372 MB), 8 of 279k x 2 heads 39 us (3.6 TB/s; the
+// take 78 us (4.7 TB/s of 372 MB), 8 of 279k x 2 heads 37 us (3.9 TB/s; the
 // shorter the call, the more of it is start, join and the last pieces' ends).
 // Short ones are latency: 531 tokens x 8 heads 9 us. A join in a launch of its
-// own took 8.5 to 20 us more; eight waves a piece 83 us for the first call above
-// but 154 instead of 118 for 256 requests of a few hundred tokens.
+// own took 8.5 to 20 us more, eight waves a piece 154 instead of 118 for 256
+// requests of 1000 tokens.
 #include "gqa_cache.h"
 
 #include <cmath>
@@ -88,27 +88,41 @@ __device__ __forceinline__ void request(const DecodeArgs& p, int b, int* start, 
   *row_tiles = (*n_q * p.g.d + kRows - 1) / kRows;
 }
 
+// n of which a call's tiles make pieces of 1 / n.
+// A segment's last piece is half a piece on average, so there are about n +
+// segs / 2 of them. Few segments: one piece a compute unit (a second does not
+// read faster, and is joined: 8 long caches 38 us, two a unit 41; 8 requests
+// with 8 new tokens 23.3 and 26). Some segments: as many as two a unit hold at
+// once (20 of up to 8000 tokens 44.6 us, one a unit 46). Many: shorter pieces
+// the more segments there are, so that the last to end are short (48 of up to
+// 8000 tokens n = 256 98 us, 320 107; 64 of them 106, n = 512 113; 100 of them
+// n = 512 175, 256 184).
+__host__ __device__ constexpr int64_t pieces_of(int64_t segs) {
+  return segs <= kNumCu / 2 ? kNumCu - segs / 2
+         : segs <= kNumCu   ? kPieces - segs
+         : segs < 3 * kNumCu ? kPieces / 2 : kPieces;
+}
+// Workgroups that n + segs pieces of at most so many segments need.
+constexpr int64_t most_groups(int64_t segs) {
+  const int64_t n = segs + pieces_of(segs);
+  return segs > kNumCu / 2 && n < kPieces ? kPieces : n;
+}
+
 // Tiles of a piece: at least all tiles over kPieces (so fewer than kPieces
 // segments have several pieces, and those fewer than 2 kPieces pieces), and at
-// least kLeast. all, segs: one lane's share of the call's tiles and segments.
-__device__ __forceinline__ int piece_tiles(const DecodeArgs& p, int64_t all, int64_t segs) {
+// least kLeast. all, segs: one lane's share of the call's tiles and segments;
+// most: the longest segment that the lane knows, then (of more than kNumCu) that
+// of all.
+__device__ __forceinline__ int piece_tiles(const DecodeArgs& p, int64_t all, int64_t segs, int* most) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
     all += __shfl_xor(all, o, 64);
     segs += __shfl_xor(segs, o, 64);
+    if (p.segs > kNumCu) *most = max(*most, __shfl_xor(*most, o, 64));
   }
   // requests whose rows overlap can exceed the grid: then nothing is cut
   if (segs > p.segs) return 1 << 30;
-  // A segment's last piece is half a piece on average, so there are about n +
-  // segs / 2 of them. Few segments: one piece a compute unit (a second does not
-  // read faster, and is joined: 8 long caches 38 us, two a unit 41; 8 requests
-  // with 8 new tokens 23.3 and 26). Some segments: as many as two a unit hold at
-  // once (20 of up to 8000 tokens 44.6 us, one a unit 46). Many: shorter pieces
-  // the more segments there are, so that the last to end are short (48 of up to
-  // 8000 tokens n = 256 98 us, 320 107; 64 of them 106, n = 512 113; 100 of them
-  // n = 512 175, 256 184).
-  const int64_t n = segs <= kNumCu / 2 ? kNumCu - segs / 2 : segs <= kNumCu ? kPieces - segs
-                    : segs < 3 * kNumCu ? kPieces / 2 : kPieces;
+  const int64_t n = pieces_of(segs);
   const int64_t c = (all + n - 1) / n;
   return c > kLeast ? static_cast<int>(c < (1 << 30) ? c : (1 << 30)) : kLeast;
 }
@@ -128,43 +142,50 @@ struct Seg {
 __device__ __forceinline__ Seg find_work(const DecodeArgs& p, int index) {
   const int lane = threadIdx.x & 63;
   int64_t all = 0, segs = 0;
-  int s, n, len, tiles, rt;
+  int s, n, len, tiles, rt, most = 0;
   for (int b0 = 0; b0 < p.B; b0 += 64) {
     request(p, b0 + lane, &s, &n, &len, &tiles, &rt);
     all += static_cast<int64_t>(tiles) * rt * p.nkv;
     segs += rt * p.nkv;
+    most = max(most, tiles);
   }
-  const int c = piece_tiles(p, all, segs);
+  const int c = piece_tiles(p, all, segs, &most);
+  // Where not all pieces run at once and some are cut, segments of half a piece
+  // or less come last, so that the last to start are short (64 ragged requests 92
+  // -> 78 us).
+  const bool late = p.segs > kNumCu && most > c && most > kAlone;
   int64_t before = 0;
-  int parts = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    if (p.B > 64) request(p, b0 + lane, &s, &n, &len, &tiles, &rt);   // else they are at hand
-    const int pieces = tiles > c && tiles > kAlone ? (tiles + c - 1) / c : 1;
-    const int seg = rt * p.nkv, groups = seg * pieces;
-    const int cut = pieces > 1 ? seg : 0;
-    int sum = groups, psum = cut * pieces;
+  for (int half = 0; half <= static_cast<int>(late); ++half) {
+    int parts = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64) {
+      if (p.B > 64) request(p, b0 + lane, &s, &n, &len, &tiles, &rt);   // else they are at hand
+      const int pieces = tiles > c && tiles > kAlone ? (tiles + c - 1) / c : 1;
+      const int seg = rt * p.nkv, groups = (late && tiles <= c / 2) == (half == 1) ? seg * pieces : 0;
+      const int cut = pieces > 1 ? seg : 0;
+      int sum = groups, psum = cut * pieces;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(sum, o, 64), v = __shfl_up(psum, o, 64);
-      if (lane >= o) sum += u, psum += v;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(sum, o, 64), v = __shfl_up(psum, o, 64);
+        if (lane >= o) sum += u, psum += v;
+      }
+      const uint64_t hit = __ballot(before + sum > index);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        Seg r;
+        r.b = b0 + l;
+        r.start = __builtin_amdgcn_readlane(s, l);
+        r.n_q = __builtin_amdgcn_readlane(n, l);
+        r.len = __builtin_amdgcn_readlane(len, l);
+        r.tiles = __builtin_amdgcn_readlane(tiles, l);
+        r.pieces = __builtin_amdgcn_readlane(pieces, l);
+        r.row_tiles = __builtin_amdgcn_readlane(rt, l);
+        r.rest = static_cast<int>(index - before) - __builtin_amdgcn_readlane(sum - groups, l);
+        r.part = parts + __builtin_amdgcn_readlane(psum - cut * pieces, l);
+        return r;
+      }
+      before += __builtin_amdgcn_readlane(sum, 63);
+      parts += __builtin_amdgcn_readlane(psum, 63);
     }
-    const uint64_t hit = __ballot(before + sum > index);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      Seg r;
-      r.b = b0 + l;
-      r.start = __builtin_amdgcn_readlane(s, l);
-      r.n_q = __builtin_amdgcn_readlane(n, l);
-      r.len = __builtin_amdgcn_readlane(len, l);
-      r.tiles = __builtin_amdgcn_readlane(tiles, l);
-      r.pieces = __builtin_amdgcn_readlane(pieces, l);
-      r.row_tiles = __builtin_amdgcn_readlane(rt, l);
-      r.rest = static_cast<int>(index - before) - __builtin_amdgcn_readlane(sum - groups, l);
-      r.part = parts + __builtin_amdgcn_readlane(psum - cut * pieces, l);
-      return r;
-    }
-    before += __builtin_amdgcn_readlane(sum, 63);
-    parts += __builtin_amdgcn_readlane(psum, 63);
   }
   return Seg{-1, 0, 0, 0, 0, 0, 0, 0, 0};
 }
@@ -553,7 +574,7 @@ int64_t segments(int B, int T, int nh, int nkv) {
 
 template <int D>
 void launch_decode(const DecodeArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(decode_kernel<D>, dim3(static_cast<unsigned>(a.segs + kPieces)), dim3(64 * NW), 0, stream, a);
+  hipLaunchKernelGGL(decode_kernel<D>, dim3(static_cast<unsigned>(most_groups(a.segs))), dim3(64 * NW), 0, stream, a);
 }
 
 }  // namespace

@@ -490,6 +490,10 @@ DECODES = [
     ([130, 9, 64], 16, 8, 2, 128, [9, 9, 4], True),
     ([500], 128, 4, 4, 64, [64], True),
     ([3, 0, 2], 16, 4, 2, 128, [3, 0, 5], False),              # nothing cached, no rows, more rows than tokens
+    # more segments than run at once, some cut, short ones last
+    ([1, 33, 5000, 700, 2, 64, 31, 0, 340], 64, 32, 32, 64, [1, 1, 1, 2, 1, 1, 1, 1, 1], False),
+    ([7 * i % 90 for i in range(66)] + [6000, 4100, 30, 2900], 32, 8, 4, 128, [1] * 70, False),
+    ([20 + i for i in range(200)], 16, 8, 4, 64, [1] * 200, False),
 ]
 
 
@@ -525,7 +529,7 @@ def test_decode_in_pieces(gpu_lib):
     torch.cuda.synchronize()
     # fp32 sums of 140000 weights: 2^-24 sqrt(n) of their size and less
     _check_decode(pg, q, [1] * 5, out, lse, fp32=1e-6, what="pieces")
-    # 40 tiles of rows over one cache: a piece has 171 tiles, a wave 43
+    # 40 tiles of rows over one cache: a piece has 371 tiles, a wave 93
     pg = Paged(6, [70000], 64, 1, 64, spare=1)
     pg.fill()
     q = _bf(pg.g.standard_normal((40, 32, 64)))
