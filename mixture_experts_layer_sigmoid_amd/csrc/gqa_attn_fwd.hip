@@ -121,13 +121,16 @@ void attn_fwd_kernel(FwdArgs p) {
   float m = -INFINITY, l = 0.f;
   const float c2 = p.scale * kLog2e;
 
-  for (int kt = first_kt; kt < n_kt; ++kt) {
+  // the two buffers' places are constants of the two calls, so that operands'
+  // addresses are an offset of the read instruction
+  auto tile = [&](int kt, auto half_c) __attribute__((always_inline)) {
+    constexpr int kHalf = decltype(half_c)::value;
     wait_vmcnt<0>();
     lds_barrier();
-    uint8_t* buf = smem + ((kt - first_kt) & 1) * kTileBytes;
-    if (kt + 1 < n_kt) load(kt + 1, smem + ((kt + 1 - first_kt) & 1) * kTileBytes);
+    const uint8_t* buf = smem + kHalf * kTileBytes;
+    if (kt + 1 < n_kt) load(kt + 1, smem + (1 - kHalf) * kTileBytes);
     const int t0 = kt * kKt;
-    if (t0 > wave_last) continue;          // nothing of this tile is visible to the wave
+    if (t0 > wave_last) return;            // nothing of this tile is visible to the wave
     f32x16_t s[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
@@ -179,6 +182,10 @@ void attn_fwd_kernel(FwdArgs p) {
           o[c] = mfma(col_operand(buf, v_off[c][0] + (2 * b + k) * 16 * RB, v_off[c][1] + (2 * b + k) * 16 * RB), pf,
                       o[c]);
       }
+  };
+  for (int kt = first_kt; kt < n_kt; kt += 2) {
+    tile(kt, std::integral_constant<int, 0>{});
+    if (kt + 1 < n_kt) tile(kt + 1, std::integral_constant<int, 1>{});
   }
   l += other_half(l);
   if constexpr (kParts) {
