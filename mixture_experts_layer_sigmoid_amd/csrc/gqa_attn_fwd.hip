@@ -163,15 +163,15 @@ void attn_fwd_kernel(FwdArgs p) {
         for (int i = 0; i < 16; ++i) o[c][i] *= a;
       m = mn;
     }
-    float sum = 0.f;
+    float sum[4] = {};
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[b][i] = exp2_hw(fmaf(s[b][i], c2, -mc));
-        sum += s[b][i];
+        sum[i & 3] += s[b][i];
       }
-    l += sum;
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
