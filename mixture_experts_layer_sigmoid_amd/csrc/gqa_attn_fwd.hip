@@ -12,13 +12,14 @@
 // product's operand without moving. The weights are rounded to bf16, as the
 // matrix instruction takes them; their sum is taken before that rounding.
 //
-// Products bound it, at the clock that the power limit leaves: 6144 queries x 64
-// heads of 128 over up to 9216 keys 660 to 690 us, 0.97 to 1.01 PFLOP/s, matrix
-// unit 54% busy at 1.7 to 2.0 GHz (an 8192^3 library product 1.22 to 1.37). Two
-// workgroups of four waves a compute unit put one wave's exponentials beside
-// another's products; within +-2% of it are eight waves a workgroup and raised
-// priorities, slower are 64 rows a wave at one wave a SIMD (709) and products
-// and softmax of neighbouring tiles interleaved in one wave (773).
+// The power limit bounds it: 6144 queries x 64 heads of 128 over up to 9216 keys
+// take 620 to 700 us, 0.95 to 1.05 PFLOP/s, with the matrix unit 55% and the
+// vector unit 49% busy at a clock of 1.67 GHz instead of 2.4 (an 8192^3 library
+// product reaches 1.22 to 1.37 PFLOP/s). Two workgroups of four waves a compute
+// unit put one wave's exponentials beside another's products; within +-2% of
+// it are eight waves a workgroup and raised priorities, slower are 64 rows a
+// wave at one wave a SIMD (709) and products and softmax of neighbouring tiles
+// interleaved in one wave (773).
 #include "gqa.h"
 
 #include <cmath>
