@@ -480,11 +480,13 @@ int waves_of(int B, int Tq, int Tk, int nh) {
   return static_cast<int64_t>(Tq) * nh >= kManyRows && Tk / B >= kLong ? 8 : 4;
 }
 // Parts that the rows of a key tile are cut into: enough workgroups for two a
-// compute unit, as far as a part keeps 4 stages of rows in the mean.
+// compute unit, as far as a part keeps 12 stages of rows in the mean (forward
+// and backward of 600 tokens x 4 heads 43 us, with 4 stages 49; 385 x 16 heads
+// 38.6 and 42; 200 x 32 heads 35 and 33).
 constexpr int kMaxParts = 32;
 int parts_of(int w, int Tq, int Tk, int nh, int nkv) {
   const int64_t wgs = (static_cast<int64_t>(Tk) + 16 * w - 1) / (16 * w) * nkv;
-  const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (32 * w);
+  const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (96 * w);
   int64_t n = 2 * kNumCu / (wgs > 0 ? wgs : 1);
   n = n < tiles ? n : tiles;
   return n < 1 ? 1 : (n > kMaxParts ? kMaxParts : static_cast<int>(n));
