@@ -21,8 +21,9 @@
 // sums are fp32.
 //
 // Seven products instead of five bound it, with the elements between them:
-// 4096 tokens in 2 sequences x 64 heads of 128 take 24 + 530 to 560 + 16 us
-// (statistics, gradients, join), 1.1 PFLOP/s of the seven, matrix unit 45% busy.
+// 4096 tokens in 2 sequences x 64 heads of 128 take 24 + 545 to 570 + 16 us
+// (statistics, gradients, join), 1.1 PFLOP/s of the seven, with the matrix unit
+// 43% and the vector unit 32% busy at a clock of 2.0 GHz.
 // One launch for both kinds: the kind with the longer workgroups goes first
 // and the other fills the units it leaves (two launches 218 + 390 us).
 #include "gqa.h"
