@@ -118,19 +118,30 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_current_stream = None      # the raw stream of torch's current one, once asked for
+
+
 def _stream(stream):
     """The raw stream of a call: torch's current one by default. (Asking for
-    the raw handle costs 0.3 us; building a torch.cuda.Stream for it 2.6 us,
+    the raw handle costs 0.2 us; building a torch.cuda.Stream for it 2.6 us,
     as much as a small kernel.)"""
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        return (_current_stream or _find_current_stream())()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _find_current_stream():
+    global _current_stream
+    import torch
+    torch.cuda.current_device()                      # initializes the GPU where nothing has yet
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream
 
 
 def _check(name: str, status: int):
