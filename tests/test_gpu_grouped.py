@@ -180,6 +180,9 @@ PACKED = [
     (8, 2, 64, [3, 20], [1500, 700], True),           # the forward's keys in parts
     (2, 1, 128, [1, 5, 2], [2100, 0, 3], False),      # parts without keys
     (12, 4, 128, [40, 7], [900, 600], False),
+    # more sequences than a wave has lanes, some empty on either side
+    (4, 2, 64, [5 * i % 11 for i in range(150)], [5 * i % 11 + i % 3 for i in range(150)], True),
+    (6, 1, 128, [i % 3 for i in range(200)], [7 * i % 90 for i in range(200)], False),
     # many rows of long sequences: the backward's larger workgroups
     (512, 16, 128, [129], [600], True),
     (256, 8, 64, [200, 0, 57], [1500, 9, 300], False),
@@ -374,6 +377,8 @@ APPENDS = [
     ([100, 5, 64], 48, 3, 128, [[60, 5, 16], [1, 0, 16], [1, 0, 31], [38, 0, 1]]),
     ([37], 32, 1, 64, [[1]] * 37),
     ([200, 200], 128, 1, 128, [[100, 3], [100, 197]]),
+    # more requests than a wave has lanes
+    ([i % 23 + i % 2 for i in range(150)], 16, 2, 64, [[i % 23 for i in range(150)], [i % 2 for i in range(150)]]),
 ]
 
 
