@@ -486,9 +486,10 @@ int waves_of(int B, int Tq, int Tk, int nh) {
 // 38.6 and 42; 200 x 32 heads 35 and 33).
 constexpr int kMaxParts = 32;
 int parts_of(int w, int Tq, int Tk, int nh, int nkv) {
+  if (Tk == 0) return 1;                                 // no dk and dv to add up: nothing for a join to do
   const int64_t wgs = (static_cast<int64_t>(Tk) + 16 * w - 1) / (16 * w) * nkv;
   const int64_t tiles = static_cast<int64_t>(Tq) * (nh / nkv) / (96 * w);
-  int64_t n = 2 * kNumCu / (wgs > 0 ? wgs : 1);
+  int64_t n = 2 * kNumCu / wgs;
   n = n < tiles ? n : tiles;
   return n < 1 ? 1 : (n > kMaxParts ? kMaxParts : static_cast<int>(n));
 }
