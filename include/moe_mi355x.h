@@ -923,15 +923,22 @@ int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q
  */
 
 /*
- * moe_gqa_append — new keys and values into the cache. A block's scale is the
- * smallest that brings the largest magnitude of the tokens it holds within
- * 448, codes are rounded to nearest even; when new tokens raise the scale, the
- * codes of the block's earlier tokens (positions before the request's new
- * ones) are rounded again under it (they keep their digits down to the codes'
- * smallest normal number, 2^-6 of the scale). Bytes of later positions are not
- * changed. So a token gives the same codes in whichever pieces its request
- * arrives, up to that second rounding. The blocks that a call writes must be
- * different ones: no page twice among them, of one request or of two.
+ * moe_gqa_append — new keys and values into the cache. A call whose new tokens
+ * start a block (its first position is among them) gives it the smallest scale
+ * that brings their largest magnitude within 448; a later call raises the scale
+ * where its new tokens need a larger one, and never lowers it. Codes are
+ * rounded to nearest even; when the scale is raised, the codes of the block's
+ * earlier tokens (positions before the request's new ones) are rounded again
+ * under it (they keep their digits down to the codes' smallest normal number,
+ * 2^-6 of the scale). Bytes of later positions are not changed. So a token
+ * gives the same codes in whichever pieces its request arrives, up to that
+ * second rounding. A request may go back: with a smaller lens the next call
+ * writes over what was there (drafted tokens that were rejected). Where it goes
+ * back into a block, the block keeps the scale that the tokens now gone had
+ * raised, and its earlier tokens their second rounding; so digits are lost
+ * below 2^-6 of that scale, less than 2^-13 of the largest magnitude the block
+ * has held, and nothing else. The blocks that a call writes must be different
+ * ones: no page twice among them, of one request or of two.
  * k, v     [T, n_kv_heads, head_dim] bf16, rows k_ld, v_ld apart. Values are
  *          expected to be finite and below 2^127: NaN and infinities become
  *          NaN codes, and an infinity brings its block to the largest scale.

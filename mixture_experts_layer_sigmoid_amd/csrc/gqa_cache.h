@@ -13,7 +13,10 @@
 // The scale is the smallest power of two that brings the block's largest
 // magnitude within 448. A finer scale would not gain: the codes have an
 // exponent of their own. A later token that raises it leaves earlier codes
-// their digits, except where they fall below the codes' normal range.
+// their digits, except where they fall below the codes' normal range. It is not
+// lowered while the block holds earlier tokens, also where a request goes back
+// over the token that raised it: the digits that the second rounding took would
+// not return.
 #pragma once
 
 #include "gqa.h"

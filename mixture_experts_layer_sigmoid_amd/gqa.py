@@ -264,7 +264,9 @@ def grouped_cache_append(k, v, cache, page_table, lens, cu, stream=None):
     """New keys and values (rotated already) [T, n_kv_heads, head_dim] bf16
     into the cache: request b's rows cu[b] .. cu[b + 1] become its last tokens,
     lens[b] (new ones included) counts them. The pages written are distinct. page_table [B, max_pages] int32,
-    lens [B] and cu [B + 1] int32."""
+    lens [B] and cu [B + 1] int32. A request that goes back (a smaller lens, to
+    write over rejected drafts) leaves the scale of the 16 tokens it goes back
+    into as large as they had made it."""
     T, kv, d = k.shape[0], cache.n_kv_heads, cache.head_dim
     if v.shape[0] != T:
         raise ValueError("as many rows of v as of k")

@@ -4,8 +4,9 @@ import pytest
 import torch
 
 import mixture_experts_layer_sigmoid_amd as moe
+from oracle import grouped as og
 from tests.gpu_util import log
-from tests.test_gpu_grouped import _bf, _cu, _i32
+from tests.test_gpu_grouped import Paged, _bf, _cu, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +34,38 @@ def test_attention_without_any_key(gpu_lib, h, kv, d, lens_q):
         assert not out.any() and not dq.any() and torch.isneginf(lse).all()
         assert dk.shape == dv.shape == (0, kv, d)
         assert (a.dk == 7).all() and (a.dv == 7).all()
+
+
+# ---- the cache ----------------------------------------------------------------------
+@pytest.mark.parametrize("d,page", [(128, 32), (64, 16)])
+def test_append_after_going_back(gpu_lib, d, page):
+    """Drafted tokens are written, rejected and written over, bit for bit: back
+    into a block it keeps the scale that they had raised, back to its first
+    position it gets one of its own."""
+    log(f"grouped append after going back D={d}")
+    pg = Paged(d, [60, 60], page, 2, d)
+    want = pg.oracle()
+    sizes = {"prompt": 1.0, "draft": 2.0 ** 9, "next": 2.0 ** -3}
+    #        what, lens after it, new tokens
+    steps = [("prompt", [21, 32], [21, 32]), ("draft", [29, 40], [8, 8]),      # 5 and 0 tokens before them
+             ("next", [24, 33], [3, 1]), ("draft", [40, 41], [16, 8]), ("next", [32, 34], [8, 1]),
+             ("next", [33, 48], [1, 14]), ("next", [17, 20], [4, 4])]
+    scales = []
+    for what, lens, new in steps:
+        k, v = (x * sizes[what] for x in pg.draw(sum(new)))
+        pg.append(lens, new, k, v)
+        torch.cuda.synchronize()
+        cu = _cu(new)
+        for name, x in (("k", k), ("v", v)):
+            for b in range(2):
+                want.append(name, x[cu[b]:cu[b + 1]].double().cpu().numpy(), pg.table[b], lens[b])
+        got = pg.oracle()
+        for name in "kv":
+            assert np.array_equal(got.codes[name], want.codes[name]), (what, name)
+            assert np.array_equal(got.e[name], want.e[name]), (what, name)
+        at = lambda b, blk: got.e["k"][pg.table[b][blk * 16 // page], :, blk * 16 % page // 16]
+        scales.append((at(0, 1), at(1, 2)))
+    prompt, draft, after = scales[:3]
+    assert (draft[0] > prompt[0]).all()
+    assert np.array_equal(after[0], draft[0]), "5 earlier tokens: kept"
+    assert (after[1] < draft[1]).all(), "no earlier token: its own"
