@@ -13,7 +13,7 @@ GroupedDecode     attention over that cache (serving): the last tokens of
 As in layer.py only marshalling happens here: shapes and types are checked,
 buffers are allocated once, every step runs in the HIP library on the given
 stream (default: torch's current one). Tensors have to be on the current
-device.
+device, and an object's buffers too.
 """
 from __future__ import annotations
 
@@ -44,6 +44,16 @@ def _here(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0 or dev != _current():
         raise ValueError(f"{name} must be on the current GPU, got {t.device}")
+    return dev
+
+
+def _beside(t: torch.Tensor, name: str, buffers: int) -> int:
+    """The same, which has to be that of the object's buffers too: the kernels
+    write to them."""
+    dev = _here(t, name)
+    if dev != buffers:
+        where = f"cuda:{buffers}" if buffers >= 0 else "the host"
+        raise ValueError(f"the object's buffers are on {where}, {name} on {t.device}")
     return dev
 
 
@@ -87,6 +97,7 @@ class QKNormRope:
         self.rotary, self.interleaved, self.eps = head_dim if rotary is None else rotary, int(interleaved), eps
         bf = dict(dtype=torch.bfloat16, device=device)
         self.q = torch.empty((T, n_heads, head_dim), **bf)
+        self.device = self.q.get_device()
         self.k = torch.empty((T, n_kv_heads, head_dim), **bf)
         self.has_backward = backward
         if backward:
@@ -99,7 +110,7 @@ class QKNormRope:
         T, h, kv, d = q.shape[0], self.n_heads, self.n_kv_heads, self.head_dim
         if T > self.T or k.shape[0] != T:
             raise ValueError(f"at most {self.T} tokens, as many rows of k as of q")
-        dev = _here(q, "q")
+        dev = _beside(q, "q", self.device)
         if w_q is not None:
             _vec(w_q, "w_q", _BF, (d,), dev)
         if w_k is not None:
@@ -164,6 +175,7 @@ class GroupedAttention:
         self.causal, self.scale = int(causal), head_dim ** -0.5 if scale is None else scale
         bf = dict(dtype=torch.bfloat16, device=device)
         self.out = torch.empty((Tq, n_heads, head_dim), **bf)
+        self.device = self.out.get_device()
         self.lse = torch.empty((Tq, n_heads), dtype=torch.float32, device=device)
         need = L.moe_gqa_attn_fwd_workspace(Tq, n_heads, head_dim)
         self.has_backward = backward
@@ -181,7 +193,7 @@ class GroupedAttention:
             raise ValueError(f"at most {self.Tq} queries and {self.Tk} keys, as many rows of v as of k")
         if not 0 <= B <= self.n_seqs:
             raise ValueError(f"cu_q must describe at most {self.n_seqs} sequences")
-        dev = _here(q, "q")
+        dev = _beside(q, "q", self.device)
         _vec(cu_q, "cu_q", _I32, (B + 1,), dev)
         _vec(cu_k, "cu_k", _I32, (B + 1,), dev)
         return (q, _rows(q, "q", h, d, dev), k, _rows(k, "k", kv, d, dev), v, _rows(v, "v", kv, d, dev),
@@ -292,6 +304,7 @@ class GroupedDecode:
         self.max_tokens, self.max_seqs = max_tokens, max_seqs
         self.scale = head_dim ** -0.5 if scale is None else scale
         self.out = torch.empty((max_tokens, n_heads, head_dim), dtype=torch.bfloat16, device=device)
+        self.device = self.out.get_device()
         # zeros once: where a call counts the pieces of its work, and leaves zeros
         self.ws = torch.zeros((L.moe_gqa_decode_workspace(head_dim),), dtype=torch.uint8, device=device)
         if self.ws.is_cuda:                # the first call may be on another stream
@@ -304,7 +317,7 @@ class GroupedDecode:
         tree_mask optional [T] int64, lse optional [T, n_heads] fp32 (filled).
         Returns out [T, n_heads, head_dim], a view of the object's buffer."""
         T, h, kv, d = q.shape[0], self.n_heads, self.n_kv_heads, self.head_dim
-        dev = _here(q, "q")
+        dev = _beside(q, "q", self.device)
         B = _requests(cache, page_table, lens, cu_q, dev)
         if T > self.max_tokens or B > self.max_seqs:
             raise ValueError(f"at most {self.max_tokens} tokens of {self.max_seqs} requests")
