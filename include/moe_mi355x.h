@@ -823,7 +823,10 @@ int moe_mla_decode(const void* q, int64_t q_ld, const void* w_uk, const void* w_
  * cos, sin [max_pos, rotary / 2] fp32, both NULL: no rotation (positions and
  *          rotary are then not used). rotary: a multiple of 16 up to head_dim.
  *          Positions [T] int32 outside [0, max_pos) take the nearest row.
- * Limits: T <= 2^23, eps in [0, 1]. T == 0 is a no-op.
+ * Limits: T <= 2^23, eps in [0, 1]. A normalized head's sum of squares has to
+ * stay below 3.4e38 (all values below 1.6e18 do) and, with eps = 0, above
+ * 1.2e-38: it is an fp32 number, and beyond them the head gives 0, infinities
+ * or NaN. T == 0 is a no-op.
  */
 int moe_qk_norm_rope(const void* q, int64_t q_ld, const void* k, int64_t k_ld, int fmt,
                      const void* w_q, const void* w_k, float eps, const float* cos,

@@ -6,9 +6,44 @@ import torch
 import mixture_experts_layer_sigmoid_amd as moe
 from oracle import grouped as og
 from tests.gpu_util import log
-from tests.test_gpu_grouped import Paged, _bf, _cu, _i32
+from tests.test_gpu_grouped import Paged, _bf, _cu, _i32, _inside, _norm_case, _np
 
 pytestmark = pytest.mark.gpu
+
+
+# ---- norms and rotation ---------------------------------------------------------
+@pytest.mark.parametrize("T,h,kv,d,rotary,il,weights", [
+    (4500, 21, 3, 128, 128, False, "qk"),   # several rounds of a token's one wave, key heads from its middle on
+    (4200, 36, 6, 64, 32, True, "qk"),
+    (4097, 10, 5, 128, 64, True, "k"),       # one token more than the backward's waves
+    (1100, 40, 8, 128, 96, False, "q"),     # two waves a token, three rounds
+])
+def test_norm_of_many_tokens(gpu_lib, T, h, kv, d, rotary, il, weights):
+    """Every row of both directions, also ones of large and small values (a
+    head's sum of squares stays below fp32's largest number)."""
+    log(f"qk norm T={T} h={h}/{kv} D={d} rotary={rotary} interleaved={il} weights={weights}")
+    q, k, w, rot, angle, g = _norm_case(T, h, kv, d, rotary, weights)
+    q[4], k[4], q[5], k[T - 1] = 1e18, -1e18, 1e-30, 0
+    eps = 1e-6
+    plan = moe.QKNormRope(T=T, n_heads=h, n_kv_heads=kv, head_dim=d, rotary=rotary, interleaved=il, eps=eps,
+                          backward=True)
+    for t in (plan.q, plan.k, plan.dq, plan.dk):
+        t.fill_(float("nan"))
+    plan.ws.fill_(255)
+    got = plan(q, k, w["q"], w["k"], **rot)
+    dy = _bf(g.standard_normal((T, h, d))), _bf(g.standard_normal((T, kv, d)))
+    grads = plan.backward(*dy, q, k, w["q"], w["k"], **rot)
+    torch.cuda.synchronize()
+    for i, (n, x) in enumerate((("q", q), ("k", k))):
+        wn = None if w[n] is None else _np(w[n])
+        want, tol = og.norm_turn(_np(x), wn, eps, angle, rotary, il)
+        _inside(_np(got[i]), want, tol + 1e-30, n)
+        dx, dtol, dw, wtol = og.norm_turn_backward(_np(dy[i]), _np(x), wn, eps, angle, rotary, il)
+        _inside(_np(grads[i]), dx, dtol + 1e-30, "d" + n)
+        if wn is None:
+            assert grads[2 + i] is None
+        else:
+            _inside(_np(grads[2 + i]), dw, wtol, "dw_" + n)
 
 
 # ---- packed sequences -------------------------------------------------------------
