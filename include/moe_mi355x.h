@@ -922,7 +922,11 @@ int moe_gqa_attn_bwd(const void* dout, int64_t dout_ld, const void* q, int64_t q
  * first rows have no place: they are not stored, and see nothing.
  * Limits: B <= 65536, B * n_kv_heads <= 2^19, T * n_kv_heads <= 2^24 (decode:
  * T * n_heads), the cache's blocks (n_pages * n_kv_heads * page_size / 16) < 2^31, page_size *
- * max_pages <= 2^30. B == 0 or T == 0 is a no-op.
+ * max_pages <= 2^30. B == 0 or T == 0 is a no-op. Beside the memory traffic a
+ * call's time has a part that grows with the square of B, which is not seen at
+ * some hundred requests; with 8 key heads and a new token each, append takes 47 us
+ * for 1024 requests and 0.5 ms for 4096, decode 0.24 ms and 3.1 ms more than its
+ * bytes, 46 ms for 16384: give larger batches in several calls.
  */
 
 /*

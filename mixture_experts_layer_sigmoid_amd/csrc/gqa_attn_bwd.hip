@@ -17,15 +17,21 @@
 //
 // p and ds are rounded to bf16 as operands of dv, dk and dq (the matrix
 // instruction's type; rms 2^-9.2 of each element). delta is formed from the
-// stored out, which is rounded to bf16; scores, dp, delta's sum and all other
-// sums are fp32.
+// stored out, which is rounded to bf16: it is the output that a caller keeps
+// anyway. An out of twice the digits beside it would take 0.1e-3 off errors of
+// 2.5e-3 to 2.8e-3 of dq and dk, for 1% of the time and twice its memory. Scores,
+// dp, delta's sum and all other sums are fp32.
 //
 // Seven products instead of five bound it, with the elements between them:
-// 4096 tokens in 2 sequences x 64 heads of 128 take 24 + 545 to 570 + 16 us
-// (statistics, gradients, join), 1.1 PFLOP/s of the seven, with the matrix unit
-// 43% and the vector unit 32% busy at a clock of 2.0 GHz.
+// 4096 tokens (2500 + 1596, causal) x 64 heads of 128 take 24 + 545 to 610 + 16 us
+// (statistics, gradients, join). The seven are 505 GFLOP: 0.83 to 0.93 PFLOP/s,
+// where a large library product reaches 1.10 to 1.37, with the matrix unit 43% and
+// the vector unit 32% busy at a clock of 2.0 GHz. With 64 values a head 12 + 370
+// to 395 + 8 us, 0.64 to 0.68 PFLOP/s (33% and 40%).
 // One launch for both kinds: the kind with the longer workgroups goes first
-// and the other fills the units it leaves (two launches 218 + 390 us).
+// and the other fills the units it leaves (in two launches dq's three products
+// 218 us, 0.99 PFLOP/s, and the four of dk and dv 390 us, 0.74: a read from LDS
+// feeds one product there, 1.7 LDS instructions a product).
 #include "gqa.h"
 
 #include <cmath>
@@ -475,7 +481,8 @@ __global__ __launch_bounds__(256) void bwd_join_kernel(BwdArgs p) {
 // sequences. Forward and backward in us, eight / four waves, 128 values a head:
 // 4096 tokens in 2 sequences x 64 heads 725 / 768, 3500 in 2 x 32 287 / 321, 1500
 // x 64 228 / 246; but 4096 x 16 400 / 363, 5 x 800 x 64 351 / 323, 8 x 300 x 64
-// 155 / 129, 512 x 128 111 / 84.
+// 155 / 129, 512 x 128 111 / 84. (64 values a head follow the same rule and were
+// not measured on both sides; the sequences' mean length counts.)
 constexpr int kManyRows = 90000, kLong = 1200;
 int waves_of(int B, int Tq, int Tk, int nh) {
   return static_cast<int64_t>(Tq) * nh >= kManyRows && Tk / B >= kLong ? 8 : 4;

@@ -13,9 +13,12 @@
 // matrix instruction takes them; their sum is taken before that rounding.
 //
 // The power limit bounds it: 6144 queries x 64 heads of 128 over up to 9216 keys
-// take 620 to 700 us, 0.95 to 1.05 PFLOP/s, with the matrix unit 55% and the
-// vector unit 49% busy at a clock of 1.67 GHz instead of 2.4 (an 8192^3 library
-// product reaches 1.22 to 1.37 PFLOP/s). Two workgroups of four waves a compute
+// take 616 to 730 us by card and run, 0.92 to 1.08 PFLOP/s, with the matrix unit
+// 55% and the vector unit 49% busy at a clock of 1.6 to 1.7 GHz instead of 2.4 (an
+// 8192^3 library product reaches 1.10 to 1.37 PFLOP/s). With 64 values a head the
+// products halve and the elements do not (11 vector instructions a product
+// instead of 6): 4000 tokens x 64 heads take 164 to 192 us, 0.68 to 0.80 PFLOP/s,
+// vector unit 62%, matrix unit 37% busy. Two workgroups of four waves a compute
 // unit put one wave's exponentials beside another's products; within +-2% of
 // it are eight waves a workgroup and raised priorities, slower are 64 rows a
 // wave at one wave a SIMD (709) and products and softmax of neighbouring tiles
@@ -253,7 +256,10 @@ __global__ __launch_bounds__(256) void fwd_join_kernel(FwdArgs p) {
 // Parts that the keys are cut into: few rows leave compute units without a
 // workgroup, then as many as fill two a unit, of at least 6 tiles in the mean
 // (16 tokens x 64 heads over 8000 keys 141 us in one part, 30 in parts of 8
-// tiles, 53 in parts of 2).
+// tiles, 53 in parts of 2: the join walks a row's parts one after another, 12 of
+// the 29 us there, 34 of 78 over 30000 keys). The mean over the sequences counts,
+// so a long one among short ones gets few parts: 16 tokens over 30000 keys packed
+// with 15 prompts of 100 take 540 us.
 constexpr int kMaxParts = 64;
 int parts_of(int B, int Tq, int Tk, int nh, int nkv) {
   const int64_t wgs = (static_cast<int64_t>(Tq) * (nh / nkv) + 32 * NW - 1) / (32 * NW) * nkv;

@@ -20,11 +20,16 @@
 // Codes times scales are exact in bf16; scores and all sums are fp32.
 //
 // Memory bounds long caches: 64 requests of 176k tokens x 8 key heads of 128
-// take 78 us (4.7 TB/s of 372 MB), 8 of 279k x 2 heads 37 us (3.9 TB/s; the
-// shorter the call, the more of it is start, join and the last pieces' ends).
-// Short ones are latency: 531 tokens x 8 heads 9 us. A join in a launch of its
-// own took 8.5 to 20 us more, eight waves a piece 154 instead of 118 for 256
-// requests of 1000 tokens.
+// take 78 to 83 us (4.5 to 4.7 TB/s of 372 MB), 8 of 279k x 2 heads 37 to 41
+// (3.5 to 3.9 TB/s; the shorter the call, the more of it is start, join and the
+// last pieces' ends). With 64 values a head a wave has half the bytes on their
+// way: 49 us (3.8 TB/s) and 22.6 (3.2). Short ones are latency: 531 tokens x 8
+// heads 9.5 us, 8.4 with 64 values. A join in a launch of its own took 8.5 to 20
+// us more, eight waves a piece 154 instead of 118 for 256 requests of 1000 tokens.
+//
+// Every wave walks through all requests to find its place, so beside the memory's
+// time a part grows with the square of their number: none is seen at 256, 1024
+// requests of 200 tokens x 8 heads take 325 us (88 for their bytes), 4096 3.5 ms.
 #include "gqa_cache.h"
 
 #include <cmath>
@@ -36,8 +41,10 @@ namespace {
 constexpr int kTok = 32;                               // cached tokens a tile
 constexpr int NW = 4;                                  // waves a workgroup
 constexpr int kRows = 32;                              // packed rows a workgroup
-// Pieces: 512 for 26 us of 8 requests with 8 new tokens x 64 heads, 768 and 1024
-// 31 and 33; 8 long caches 41, 47 and 45; 64 requests the same within 3%.
+// The most that pieces_of gives, two a compute unit; it sizes the workspace. (With
+// one number for all calls 512 was the best: 768 and 1024 19 and 27% slower for
+// 8 requests with 8 new tokens, 15 and 10% for 8 long caches, 64 requests the same
+// within 3%. pieces_of's own numbers are below.)
 constexpr int kPieces = 2 * kNumCu;                    // pieces beside one a (request, head, rows)
 constexpr int kParts = 2 * kPieces;                    // pieces of segments that have several, at most
 // 4 requests of 8000 tokens with 4 new each: pieces of at least 2 NW, 4 NW and

@@ -13,10 +13,10 @@
 // pairs, so a rotation needs no exchange. A wave's groups of lanes walk the
 // heads of one token, whose angles stay in registers.
 //
-// Memory bounds both: 8192 tokens x (64 + 8) heads of 128 take 64 us forward for
-// 302 MB (4.7 TB/s) and 107 + 4.7 us backward for 453 MB (4.2 TB/s; the weights'
-// gradients are summed in registers over a workgroup's tokens and in a second
-// launch over the workgroups, so they repeat bit for bit).
+// Memory bounds both: 8192 tokens x (64 + 8) heads of 128 take 61 to 65 us forward
+// for 302 MB (4.6 to 4.9 TB/s) and 106 to 110 + 4.8 us backward for 453 MB (4.1 to
+// 4.3 TB/s; the weights' gradients are summed in registers over a workgroup's
+// tokens and in a second launch over the workgroups, so they repeat bit for bit).
 #include "gqa.h"
 
 #include <cmath>
